@@ -1,5 +1,6 @@
 """Python binding of libpn.so (C ABI in include/pn.h): PN (pn3t / pn4t) and NVFP4 W4A16
-decode-step GEMV, validation, decode and quantizers on MI355X (gfx950).
+decode-step GEMV, validation, decode and quantizers, the microscaled key/value cache with the
+attention that reads it, and the verification of drafted tokens, on MI355X (gfx950).
 
 Argument marshalling only: every step runs in the HIP kernels of libpn.so. PyTorch supplies device
 memory and the current stream. There is no CPU fallback: if the library is missing, importing
@@ -14,6 +15,8 @@ __all__ = ["PN3T", "PN4T", "PNError", "row_bytes", "validate_rows", "validate_ro
            "dequantize_rows", "dequantize_row", "gemv", "gemv_group", "quantize_rows", "hadamard_rows",
            "gemv_hadamard", "gemv_hadamard_noalloc", "gemv_group_hadamard", "nvfp4_validate_rows",
            "nvfp4_dequantize_rows", "gemv_nvfp4", "fp8row_validate_rows", "fp8row_dequantize_rows", "gemv_fp8row",
+           "MXFP8", "MXFP4", "Cache", "cache_page_bytes", "cache_write", "cache_read",
+           "attend_workspace_bytes", "attend", "verify_workspace_bytes", "verify",
            "library_path", "status_string", "lib"]
 
 PN3T = 124
@@ -24,6 +27,9 @@ GEMV_MAX_TOKENS = 16   # PN GEMV
 GEMV_HADAMARD_MAX_TOKENS = 4  # PN GEMV with the rotation fused
 GEMV_GROUP_MAX_PARTS = 4  # matrices per pn_gemv_group call
 NOALLOC_MAX_FLOATS = 262144  # M * K limit of pn_gemv_hadamard_noalloc
+MXFP8 = 0              # cache formats
+MXFP4 = 1
+VERIFY_MAX_DRAFTS = 63
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libpn.so")
@@ -38,6 +44,22 @@ _P, _I64, _I32, _F = C.c_void_p, C.c_int64, C.c_int, C.c_float
 class GemvPart(C.Structure):
     """pn_gemv_part of include/pn.h: one matrix of a pn_gemv_group call."""
     _fields_ = [("type", C.c_int), ("W", C.c_void_p), ("N", C.c_int64), ("y", C.c_void_p)]
+
+
+class CacheDesc(C.Structure):
+    """pn_cache of include/pn.h."""
+    _fields_ = [("format", C.c_int), ("heads", C.c_int), ("dim", C.c_int), ("page", C.c_int),
+                ("pages", C.c_int64), ("data", C.c_void_p)]
+
+
+class AttendArgs(C.Structure):
+    """pn_attend_args of include/pn.h."""
+    _fields_ = [("type", C.c_int), ("B", C.c_int), ("Q", C.c_int), ("Hq", C.c_int),
+                ("q", C.c_void_p), ("q_seq_stride", C.c_int64), ("q_token_stride", C.c_int64),
+                ("q_head_stride", C.c_int64), ("scale", C.c_float), ("table", C.c_void_p),
+                ("table_stride", C.c_int64), ("table_width", C.c_int), ("lens", C.c_void_p),
+                ("q_lens", C.c_void_p), ("prefix_table", C.c_void_p), ("prefix_len", C.c_int64),
+                ("out", C.c_void_p), ("lse", C.c_void_p)]
 
 
 _SIGS = {
@@ -60,6 +82,14 @@ _SIGS = {
     "pn_fp8row_validate_rows": (_I32, [_P, _P, _I64, _I64, _P, _P]),
     "pn_fp8row_dequantize_rows": (_I32, [_P, _P, _I64, _I64, _P, _P]),
     "pn_gemv_fp8row": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "pn_cache_page_bytes": (_I64, [_I32, _I32, _I32, _I32]),
+    "pn_cache_write": (_I32, [_P, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P]),
+    "pn_cache_read": (_I32, [_P, _I32, _P, _I64, _P, _P, _P]),
+    "pn_attend_workspace_bytes": (_I64, [_P, _P]),
+    "pn_attend": (_I32, [_P, _P, _P, _I64, _P]),
+    "pn_verify_workspace_bytes": (_I64, [_I64, _I64]),
+    "pn_verify": (_I32, [_I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P,
+                         _I64, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -297,3 +327,184 @@ def gemv_fp8row_ptr(codes_ptr, scales_ptr, N, K, x_ptr, M, y_ptr, stream_handle)
     return _lib.pn_gemv_fp8row(codes_ptr, scales_ptr, N, K, x_ptr, M, y_ptr, stream_handle)
 
 
+# ---- microscaled cache, attention over it, verification of drafts ---------------------------------
+
+_TYPE_OF = {}
+
+
+def _elem(t, name):
+    """The element type id of a plain tensor on the device."""
+    if not _TYPE_OF:
+        import torch
+        _TYPE_OF.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in _TYPE_OF:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _TYPE_OF[t.dtype]
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _ints(t, name, dtype, shape):
+    import torch
+    _dev(t, name, getattr(torch, dtype))
+    _shape(t, name, shape)
+
+
+def cache_page_bytes(format, heads, dim, page):
+    """Bytes of one page of a cache (pn_cache_page_bytes); 0 where the library has no such cache."""
+    return int(_lib.pn_cache_page_bytes(format, heads, dim, page))
+
+
+class Cache:
+    """A paged microscaled key/value cache over `data`, a contiguous uint8 device tensor of whole pages
+    (cache_page_bytes each). Token places are slots: page number * page + place in the page. The bytes
+    need no initial value: only tokens that were written are ever used."""
+
+    def __init__(self, format, heads, dim, page, data):
+        import torch
+        each = cache_page_bytes(format, heads, dim, page)
+        if each == 0:
+            raise ValueError(f"no cache of format {format} with {heads} heads of {dim} channels and "
+                             f"pages of {page} tokens")
+        _dev(data, "data", torch.uint8)
+        if data.numel() % each:
+            raise ValueError(f"data must be whole pages of {each} bytes, got {data.numel()}")
+        self.format, self.heads, self.dim, self.page = format, heads, dim, page
+        self.pages, self.data = data.numel() // each, data
+        self.desc = CacheDesc(format, heads, dim, page, self.pages, data.data_ptr())
+        self.ref = C.addressof(self.desc)
+
+
+def cache_write(cache, k, v, slots, stream=None):
+    """Quantises k and v [T, heads, dim] (channels contiguous) into the cache; token t goes to
+    slots[t] (int64), nowhere where that is outside the cache (pn_cache_write)."""
+    kind = _elem(k, "k")
+    shape = (k.shape[0], cache.heads, cache.dim)
+    _shape(k, "k", shape)
+    _shape(v, "v", shape)
+    if _elem(v, "v") != kind:
+        raise ValueError("k and v must have the same type")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("the channels of k and v must be contiguous")
+    _ints(slots, "slots", "int64", shape[:1])
+    _check(_lib.pn_cache_write(cache.ref, kind, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+                               v.stride(0), v.stride(1), slots.data_ptr(), shape[0], _stream(stream)),
+           "pn_cache_write")
+
+
+def cache_read(cache, slots, k, v, stream=None):
+    """k and v [T, heads, dim] <- the cache's tokens at slots (int64); zeros for a slot outside it
+    (pn_cache_read)."""
+    kind = _elem(k, "k")
+    shape = (slots.shape[0], cache.heads, cache.dim)
+    _ints(slots, "slots", "int64", shape[:1])
+    _dev(k, "k")
+    _dev(v, "v", k.dtype)
+    _shape(k, "k", shape)
+    _shape(v, "v", shape)
+    _check(_lib.pn_cache_read(cache.ref, kind, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+                              _stream(stream)), "pn_cache_read")
+
+
+def attend_workspace_bytes(cache, q, table, prefix_len=0):
+    """Device bytes that attend needs for q [B, Q, Hq, dim] and these tables."""
+    B, Q, Hq, _ = q.shape
+    a = AttendArgs(type=_elem(q, "q"), B=B, Q=Q, Hq=Hq, scale=1.0, table_width=table.shape[1],
+                   prefix_len=prefix_len)
+    return int(_lib.pn_attend_workspace_bytes(cache.ref, C.addressof(a)))
+
+
+def attend(cache, q, table, lens, out, lse=None, workspace=None, prefix_table=None, prefix_len=0,
+           q_lens=None, scale=None, stream=None):
+    """out [B, Q, Hq, dim] <- attention of q [B, Q, Hq, dim] (any strides, channels contiguous) over the
+    first prefix_len tokens of the pages in prefix_table (int32), which every sequence sees, and over
+    each sequence's own tokens: lens int32[B], in the pages of table int32[B, width] (pn_attend). The
+    last of the own tokens are the queries', each sees up to itself. lse fp32[B, Q, Hq] <- the log of
+    the sum of exp(scores). q_lens int32[B]: query tokens that a sequence has, Q unless given. scale:
+    dim ** -0.5 unless given. workspace: a uint8 tensor of attend_workspace_bytes."""
+    kind = _elem(q, "q")
+    if q.dim() != 4 or q.shape[3] != cache.dim:
+        raise ValueError(f"q must be [B, Q, Hq, {cache.dim}], got {tuple(q.shape)}")
+    B, Q, Hq, _ = q.shape
+    qs = q.stride()
+    if qs[3] != 1:
+        raise ValueError("the channels of q must be contiguous")
+    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be [{B}, width] with contiguous rows, got {tuple(table.shape)}")
+    import torch
+    if table.dtype != torch.int32 or not table.is_cuda:
+        raise ValueError("table must be an int32 device tensor")
+    _ints(lens, "lens", "int32", (B,))
+    _dev(out, "out", q.dtype)
+    _shape(out, "out", q.shape)
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+        _shape(lse, "lse", (B, Q, Hq))
+    if q_lens is not None:
+        _ints(q_lens, "q_lens", "int32", (B,))
+    if prefix_len < 0:
+        raise ValueError("prefix_len must not be negative")
+    if prefix_len:
+        _dev(prefix_table, "prefix_table", torch.int32)
+        if prefix_table.numel() * cache.page < prefix_len:
+            raise ValueError("prefix_table has too few pages for prefix_len")
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+    a = AttendArgs(kind, B, Q, Hq, q.data_ptr(), qs[0], qs[1], qs[2],
+                   cache.dim ** -0.5 if scale is None else scale, table.data_ptr(), table.stride(0),
+                   table.shape[1], lens.data_ptr(), _ptr(q_lens), _ptr(prefix_table), prefix_len,
+                   out.data_ptr(), _ptr(lse))
+    _check(_lib.pn_attend(cache.ref, C.addressof(a), _ptr(workspace),
+                          0 if workspace is None else workspace.numel(), _stream(stream)), "pn_attend")
+
+
+def verify_workspace_bytes(B, V):
+    """Device bytes that verify needs for B sequences over V tokens."""
+    return int(_lib.pn_verify_workspace_bytes(B, V))
+
+
+def verify(p, q, draft, u_accept, u_sample, tokens, accepted, workspace, n_draft=None, stream=None):
+    """Drafted tokens against the target's probabilities (pn_verify): p [B, K + 1, V] the target's, q
+    [B, K, V] the draft's (None where each draft was certain), rows of any even spacing; draft
+    int32[B, K], u_accept fp32[B, K] and u_sample fp32[B] random numbers in [0, 1); tokens
+    int32[B, K + 1] <- the accepted drafts, the token after them, then -1; accepted int32[B] <- their
+    number. n_draft int32[B]: drafts that a sequence has, K unless given. workspace: a uint8 tensor
+    of verify_workspace_bytes."""
+    import torch
+    kind = _elem(p, "p")
+    B, K = draft.shape
+    if p.dim() != 3 or p.shape[0] != B or p.shape[1] != K + 1:
+        raise ValueError(f"p must be [{B}, {K + 1}, V], got {tuple(p.shape)}")
+    V = p.shape[2]
+
+    def rows(t, name, n):
+        if t.stride(2) != 1 or (B > 1 and t.stride(0) != n * t.stride(1)):
+            raise ValueError(f"the rows of {name} must be contiguous and evenly spaced")
+        return t.stride(1) if n > 1 else t.stride(0)
+    ps = rows(p, "p", K + 1)
+    qs = 0
+    if q is not None:
+        if _elem(q, "q") != kind:
+            raise ValueError("p and q must have the same type")
+        _shape(q, "q", (B, K, V))
+        if K:
+            qs = rows(q, "q", K)
+    _ints(draft, "draft", "int32", (B, K))
+    _dev(u_accept, "u_accept", torch.float32)
+    _shape(u_accept, "u_accept", (B, K))
+    _dev(u_sample, "u_sample", torch.float32)
+    _shape(u_sample, "u_sample", (B,))
+    _ints(tokens, "tokens", "int32", (B, K + 1))
+    _ints(accepted, "accepted", "int32", (B,))
+    if n_draft is not None:
+        _ints(n_draft, "n_draft", "int32", (B,))
+    _dev(workspace, "workspace", torch.uint8)
+    _check(_lib.pn_verify(kind, p.data_ptr(), ps, _ptr(q) if K else 0, qs, draft.data_ptr(), _ptr(n_draft),
+                          u_accept.data_ptr(), u_sample.data_ptr(), B, K, V, tokens.data_ptr(),
+                          accepted.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                          _stream(stream)), "pn_verify")

@@ -1,0 +1,143 @@
+// pn_attend.hip -- pn_attend's arguments, how a call is cut into workgroups, and its entry points.
+// The kernels are in pn_attend.h.
+#include "pn_attend.h"
+
+namespace pn {
+
+template <>
+int launch_format<PN_CACHE_MXFP8>(const AttendArgs &A, int dim, bool two, int rp, int ro, hipStream_t s);
+template <>
+int launch_format<PN_CACHE_MXFP4>(const AttendArgs &A, int dim, bool two, int rp, int ro, hipStream_t s);
+
+// How a call is cut: rows a wave holds, row blocks and token ranges.
+struct Cut {
+    int rp, ro;  // tiles of 16 rows (prefix, own)
+    int prefix_splits, prefix_blocks, own_splits, own_blocks;
+    bool direct;
+    int64_t rows;
+    int64_t workspace;
+};
+
+static int attend_check(const pn_cache *cache, const pn_attend_args *a, CacheView &c)
+{
+    const int st = cache_view(cache, c);
+    if (st != PN_OK)
+        return st;
+    if (!a)
+        return PN_ERR_NULL;
+    if (elem_bytes(a->type) == 0)
+        return PN_ERR_FORMAT;
+    const int64_t most = INT32_MAX - 64;  // tokens, rows and workgroups are counted in 32 bits
+    if (a->B < 0 || a->Q < 0 || a->Hq < 1 || a->Hq % cache->heads || a->table_width < 0 ||
+        a->prefix_len < 0 || a->prefix_len > most || (int64_t)a->table_width * cache->page > most ||
+        !isfinite(a->scale))
+        return PN_ERR_SHAPE;
+    if ((int64_t)a->B * a->Q > most / a->Hq)
+        return PN_ERR_SHAPE;
+    return PN_OK;
+}
+
+static Cut attend_cut(const pn_cache *cache, const pn_attend_args *a)
+{
+    const int G = a->Hq / cache->heads;
+    const bool two = a->type != PN_BF16;
+    Cut t;
+    const int64_t own_rows = (int64_t)a->Q * G, prefix_rows = own_rows * a->B;
+    const int64_t own_records = (int64_t)a->table_width * (cache->page / kTile);
+    const int64_t prefix_records = (a->prefix_len + kTile - 1) / kTile;
+    t.ro = own_rows <= 16 ? 1 : 2;
+    t.rp = prefix_records == 0 ? 0 : prefix_rows <= 16 ? 1 : cache->dim == 256 || two ? 2 : 4;
+    t.own_blocks = (int)((own_rows + 16 * t.ro - 1) / (16 * t.ro));
+    t.prefix_blocks = t.rp ? (int)((prefix_rows + 16 * t.rp - 1) / (16 * t.rp)) : 0;
+    // two workgroups a CU, at least one record a wave
+    const int64_t want = 2 * device_cus();
+    auto splits = [&](int64_t items, int64_t records) {
+        return (int)std::max<int64_t>(1, std::min((want + items - 1) / items, (records + 3) / 4));
+    };
+    t.own_splits = splits((int64_t)a->B * cache->heads * t.own_blocks, own_records);
+    t.prefix_splits = t.rp ? splits((int64_t)cache->heads * t.prefix_blocks, prefix_records) : 0;
+    t.direct = t.own_splits + t.prefix_splits == 1;
+    t.rows = (int64_t)a->B * a->Q * a->Hq;
+    t.workspace = t.direct ? 0 : (t.own_splits + t.prefix_splits) * t.rows * (cache->dim + 2) * 4;
+    return t;
+}
+
+}  // namespace pn
+
+using namespace pn;
+
+extern "C" int64_t pn_attend_workspace_bytes(const pn_cache *cache, const pn_attend_args *a)
+{
+    CacheView c;
+    if (attend_check(cache, a, c) != PN_OK || a->B == 0 || a->Q == 0)
+        return 0;
+    return attend_cut(cache, a).workspace;
+}
+
+extern "C" int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *workspace,
+                         int64_t workspace_bytes, void *stream)
+{
+    CacheView c;
+    int st = attend_check(cache, a, c);
+    if (st != PN_OK)
+        return st;
+    if (a->B == 0 || a->Q == 0)
+        return PN_OK;
+    const int size = elem_bytes(a->type);
+    if (!a->q || !a->out || !a->lens || (a->table_width > 0 && !a->table) ||
+        (a->prefix_len > 0 && !a->prefix_table))
+        return PN_ERR_NULL;
+    if (!aligned(a->q, size) || !aligned(a->out, 16) || !aligned(a->lens, 4) ||
+        !aligned(a->table, 4) || !aligned(a->prefix_table, 4) || !aligned(a->q_lens, 4) ||
+        !aligned(a->lse, 4))
+        return PN_ERR_ALIGN;
+    if (c.pages == 0 && (a->table_width > 0 || a->prefix_len > 0))
+        return PN_ERR_SHAPE;  // no page to read
+    const Cut t = attend_cut(cache, a);
+    if (t.workspace > 0) {
+        if (!workspace)
+            return PN_ERR_NULL;
+        if (!aligned(workspace, 16))
+            return PN_ERR_ALIGN;
+        if (workspace_bytes < t.workspace)
+            return PN_ERR_WORKSPACE;
+    }
+    if ((st = check_device()) != PN_OK)
+        return st;
+    AttendArgs A;
+    A.c = c;
+    A.type = a->type;
+    A.B = a->B;
+    A.Q = a->Q;
+    A.Hq = a->Hq;
+    A.G = a->Hq / cache->heads;
+    A.q = a->q;
+    A.q_seq = a->q_seq_stride;
+    A.q_tok = a->q_token_stride;
+    A.q_head = a->q_head_stride;
+    const int eight = size * 8 > 16 ? 4 : 8;  // elements of 16 bytes
+    A.q_vec = aligned(a->q, 16) && ((A.q_seq | A.q_tok | A.q_head) & (eight - 1)) == 0;
+    A.scale = fmaxf(fabsf(a->scale) * kLog2e, 0x1p-126f);
+    A.neg = a->scale < 0.0f;
+    A.table = a->table;
+    A.table_stride = a->table_stride;
+    A.table_width = a->table_width;
+    A.lens = a->lens;
+    A.q_lens = a->q_lens;
+    A.prefix_table = a->prefix_table;
+    A.prefix_len = (int)a->prefix_len;
+    A.prefix_splits = t.prefix_splits;
+    A.prefix_blocks = t.prefix_blocks;
+    A.own_splits = t.own_splits;
+    A.own_blocks = t.own_blocks;
+    A.direct = t.direct;
+    A.part = (float *)workspace;
+    A.part_ml = (float2 *)((float *)workspace + (int64_t)(t.own_splits + t.prefix_splits) * t.rows * cache->dim);
+    A.out = a->out;
+    A.lse = a->lse;
+    hipStream_t s = (hipStream_t)stream;
+    const bool two = a->type != PN_BF16;
+    return cache->format == PN_CACHE_MXFP8
+               ? launch_format<PN_CACHE_MXFP8>(A, cache->dim, two, t.rp, t.ro, s)
+               : launch_format<PN_CACHE_MXFP4>(A, cache->dim, two, t.rp, t.ro, s);
+}

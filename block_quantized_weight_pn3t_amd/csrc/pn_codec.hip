@@ -209,6 +209,8 @@ const char *pn_status_string(int status)
     case PN_ERR_HIP: return "HIP runtime error";
     case PN_ERR_DEVICE: return "current device is not gfx950";
     case PN_ERR_HADAMARD: return "Hadamard slice size is not a power of two in 2..16384 dividing K";
+    case PN_ERR_FORMAT: return "unknown cache format or element type";
+    case PN_ERR_WORKSPACE: return "workspace too small";
     default: return "unknown status";
     }
 }

@@ -1,0 +1,332 @@
+// pn_verify.hip -- drafted tokens verified against the target's probabilities, on gfx950.
+//
+// Draft i stands iff all before it do and u_i q_i(x_i) < p_i(x_i); after a accepted drafts the next
+// token is drawn from r = max(p_a - q_a, 0) (p_a after the last draft, or where r is zero) by
+// inversion: the first t with r_0 + .. + r_t > u R. Probabilities are fp32 at most, so u q is exact
+// in 64 bits, and differences and sums are taken there: their rounding (2^-53 a step) is far below
+// what separates two tokens.
+//
+// Memory bound: one row of p and one of q a sequence. The rows are too long for one workgroup (a
+// single CU reads a small part of what the memory gives), so they are cut into chunks of kChunk:
+//   verify_sums    a workgroup a chunk: every wave works out the accepted count by itself (a lane a
+//                  draft, one ballot), then the chunk's sums of r and of p go to the workspace
+//   verify_choose  a workgroup a sequence: the chunk in which the running sum passes u R, then the
+//                  token inside it, from LDS
+#include <algorithm>
+
+#include "pn_cache.h"
+
+namespace pn {
+
+constexpr int kChunk = 2048;        // numbers of a row a workgroup sums
+constexpr int kPer = kChunk / 256;  // of those, a thread's
+
+struct VerifyArgs {
+    const void *p, *q;
+    int64_t p_stride, q_stride;
+    const int32_t *draft, *n_draft;
+    const float *u_accept, *u_sample;
+    int64_t V;
+    int K, chunks;
+    int32_t *tokens, *accepted;
+    double2 *sums;  // [sequence][chunk]: r, p
+};
+
+template <int T>
+__device__ __forceinline__ double prob(const void *p, int64_t at)
+{
+    return (double)(float)reinterpret_cast<const typename Elem<T>::type *>(p)[at];
+}
+
+// r of one token (NaN and negative numbers count as 0)
+__device__ __forceinline__ double rest(double p, double q) { return p > q ? p - q : 0.0; }
+__device__ __forceinline__ double positive(double p) { return p > 0.0 ? p : 0.0; }
+
+// How a sequence's next token is drawn: rows of p and q (one < 0: no row of q), and the draft that a
+// certain q takes out of p (-1: none).
+struct Draw {
+    int64_t p_row, q_row;
+    int out;
+};
+__device__ __forceinline__ Draw draw_of(const VerifyArgs &A, int64_t b, int a, int n)
+{
+    Draw d;
+    d.p_row = (b * (A.K + 1) + a) * A.p_stride;
+    d.q_row = a < n && A.q ? (b * A.K + a) * A.q_stride : -1;
+    d.out = a < n && !A.q ? A.draft[b * A.K + a] : -1;
+    return d;
+}
+__device__ __forceinline__ int drafts_of(const VerifyArgs &A, int64_t b)
+{
+    return A.n_draft ? min(max(A.n_draft[b], 0), A.K) : A.K;
+}
+
+// Sum over the workgroup's 256 threads, in every thread.
+__device__ __forceinline__ double group_sum(double v, double *lds)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        v += __shfl_xor(v, o, 64);
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    __syncthreads();
+    return v;
+}
+
+template <int T>
+__global__ void __launch_bounds__(256) verify_sums(VerifyArgs A)
+{
+    typedef typename Elem<T>::type E;
+    constexpr int VEC = 16 / sizeof(E);
+    typedef E EV __attribute__((ext_vector_type(VEC)));
+    __shared__ double lds[4];
+    const int64_t b = blockIdx.x / (unsigned)A.chunks;
+    const int chunk = (int)(blockIdx.x - b * A.chunks);
+    const int lane = threadIdx.x & 63;
+    const int n = drafts_of(A, b);
+
+    bool ok = false;
+    int x = -1;
+    if (lane < n) {
+        x = A.draft[b * A.K + lane];
+        if (x >= 0 && x < A.V) {
+            const double px = prob<T>(A.p, (b * (A.K + 1) + lane) * A.p_stride + x);
+            const double qx = A.q ? prob<T>(A.q, (b * A.K + lane) * A.q_stride + x) : 1.0;
+            ok = (double)A.u_accept[b * A.K + lane] * qx < px;
+        }
+    }
+    const int a = __ffsll((unsigned long long)~__ballot(ok)) - 1;  // n <= 63: some lane is false
+    if (chunk == 0 && threadIdx.x < 64) {
+        if (lane <= A.K && lane != a)
+            A.tokens[b * (A.K + 1) + lane] = lane < a ? x : -1;
+        if (lane == 0)
+            A.accepted[b] = a;
+    }
+
+    const Draw d = draw_of(A, b, a, n);
+    const E *const p = reinterpret_cast<const E *>(A.p) + d.p_row;
+    const E *const q = d.q_row < 0 ? nullptr : reinterpret_cast<const E *>(A.q) + d.q_row;
+    const int64_t base = (int64_t)chunk * kChunk;
+    double sr = 0.0, sp = 0.0;
+    if (base + kChunk <= A.V && (((uintptr_t)p | (uintptr_t)q) & 15) == 0) {
+        EV pv[kPer / VEC], qv[kPer / VEC];
+#pragma unroll
+        for (int k = 0; k < kPer / VEC; k++) {
+            pv[k] = *reinterpret_cast<const EV *>(p + base + (k * 256 + threadIdx.x) * VEC);
+            qv[k] = q ? *reinterpret_cast<const EV *>(q + base + (k * 256 + threadIdx.x) * VEC) : EV(0);
+        }
+#pragma unroll
+        for (int k = 0; k < kPer / VEC; k++)
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                const double pt = (double)(float)pv[k][e];
+                const bool out = base + (k * 256 + threadIdx.x) * VEC + e == d.out;
+                sr += out ? 0.0 : rest(pt, (double)(float)qv[k][e]);
+                sp += positive(pt);
+            }
+    } else {
+        E pv[kPer], qv[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; k++) {
+            const int64_t t = base + k * 256 + threadIdx.x;
+            pv[k] = t < A.V ? p[t] : (E)0.0f;
+            qv[k] = t < A.V && q ? q[t] : (E)0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; k++) {
+            const double pt = (double)(float)pv[k];
+            sr += base + k * 256 + threadIdx.x == d.out ? 0.0 : rest(pt, (double)(float)qv[k]);
+            sp += positive(pt);
+        }
+    }
+    sr = group_sum(sr, lds);
+    sp = group_sum(sp, lds);
+    if (threadIdx.x == 0)
+        A.sums[blockIdx.x] = make_double2(sr, sp);
+}
+
+// The sum of the threads before this one, and all of them; lds[0..3] is scratch.
+__device__ __forceinline__ double before(double v, double *lds, double &all)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double s = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double t = __shfl_up(s, o, 64);
+        if (lane >= o)
+            s += t;
+    }
+    if (lane == 63)
+        lds[wave] = s;
+    __syncthreads();
+    double base = 0.0;
+#pragma unroll
+    for (int w = 0; w < 3; w++)
+        if (w < wave)
+            base += lds[w];
+    all = ((lds[0] + lds[1]) + lds[2]) + lds[3];
+    __syncthreads();
+    const double prev = __shfl_up(s, 1, 64);
+    return base + (lane ? prev : 0.0);
+}
+
+// The least (or greatest) of the workgroup's values.
+__device__ __forceinline__ int group_least(int v, int *lds)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        v = min(v, __shfl_xor(v, o, 64));
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = min(min(lds[0], lds[1]), min(lds[2], lds[3]));
+    __syncthreads();
+    return v;
+}
+
+template <int T>
+__global__ void __launch_bounds__(256) verify_choose(VerifyArgs A)
+{
+    __shared__ double lds[4];
+    __shared__ int least[4];
+    __shared__ double run[kChunk];
+    __shared__ double chosen_before;
+    const int64_t b = blockIdx.x;
+    const int n = drafts_of(A, b), a = A.accepted[b];
+    const double2 *const sums = A.sums + b * A.chunks;
+
+    // each thread has a run of chunks
+    const int each = (A.chunks + 255) / 256;
+    const int c0 = min(A.chunks, (int)threadIdx.x * each), c1 = min(A.chunks, c0 + each);
+    double r = 0.0, p = 0.0;
+    for (int c = c0; c < c1; c++) {
+        r += sums[c].x;
+        p += sums[c].y;
+    }
+    double all_r, all_p;
+    const double before_r = before(r, lds, all_r), before_p = before(p, lds, all_p);
+    const bool whole = !(all_r > 0.0);  // r is zero everywhere: draw from p
+    const double total = whole ? all_p : all_r;
+    int64_t token = -1;
+    if (total > 0.0) {
+        const double at = (double)A.u_sample[b] * total;
+        // the first chunk that passes `at`; if none, the last that has anything
+        double sum = whole ? before_p : before_r, found = 0.0;
+        int first = INT32_MAX, last = -1;
+        for (int c = c0; c < c1; c++) {
+            const double s = whole ? sums[c].y : sums[c].x;
+            if (s > 0.0) {
+                last = c;
+                if (first == INT32_MAX && sum + s > at) {
+                    first = c;
+                    found = sum;
+                }
+            }
+            sum += s;
+        }
+        int chunk = group_least(first, least);
+        const bool passed = chunk != INT32_MAX;
+        if (!passed)
+            chunk = -group_least(-last, least);
+        if (passed && first == chunk)
+            chosen_before = found;
+
+        const Draw d = draw_of(A, b, a, n);
+        const int64_t base = (int64_t)chunk * kChunk;
+        for (int k = threadIdx.x; k < kChunk; k += 256) {
+            const int64_t t = base + k;
+            double v = 0.0;
+            if (t < A.V) {
+                const double pt = prob<T>(A.p, d.p_row + t);
+                if (whole)
+                    v = positive(pt);
+                else if (t != d.out)
+                    v = rest(pt, d.q_row < 0 ? 0.0 : prob<T>(A.q, d.q_row + t));
+            }
+            run[k] = v;
+        }
+        __syncthreads();
+        double mine = 0.0, all;
+#pragma unroll
+        for (int k = 0; k < kPer; k++)
+            mine += run[threadIdx.x * kPer + k];
+        sum = before(mine, lds, all) + (passed ? chosen_before : 0.0);
+        first = INT32_MAX;
+        last = -1;
+#pragma unroll
+        for (int k = 0; k < kPer; k++) {
+            const int t = threadIdx.x * kPer + k;
+            const double v = run[t];
+            sum += v;
+            if (v > 0.0) {
+                last = t;
+                if (passed && first == INT32_MAX && sum > at)
+                    first = t;
+            }
+        }
+        int t = group_least(first, least);
+        if (t == INT32_MAX)
+            t = -group_least(-last, least);
+        token = base + t;
+    }
+    if (threadIdx.x == 0)
+        A.tokens[b * (A.K + 1) + a] = (int32_t)token;
+}
+
+template <int T>
+static int launch_verify(const VerifyArgs &A, int64_t B, hipStream_t s)
+{
+    hipLaunchKernelGGL((verify_sums<T>), dim3((unsigned)(B * A.chunks)), dim3(256), 0, s, A);
+    const int st = launch_status();
+    if (st != PN_OK)
+        return st;
+    hipLaunchKernelGGL((verify_choose<T>), dim3((unsigned)B), dim3(256), 0, s, A);
+    return launch_status();
+}
+
+static int64_t verify_chunks(int64_t V) { return (V + kChunk - 1) / kChunk; }
+
+}  // namespace pn
+
+using namespace pn;
+
+extern "C" int64_t pn_verify_workspace_bytes(int64_t B, int64_t V)
+{
+    if (B < 0 || V < 1 || V >= (int64_t)1 << 30 || B > INT32_MAX / verify_chunks(V))
+        return 0;
+    return B * verify_chunks(V) * (int64_t)sizeof(double2);
+}
+
+extern "C" int pn_verify(int type, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                         const int32_t *draft, const int32_t *n_draft, const float *u_accept,
+                         const float *u_sample, int64_t B, int64_t K, int64_t V, int32_t *tokens,
+                         int32_t *accepted, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int size = elem_bytes(type);
+    if (size == 0)
+        return PN_ERR_FORMAT;
+    if (B < 0 || K < 0 || K > PN_VERIFY_MAX_DRAFTS || V < 1 || V >= (int64_t)1 << 30 ||
+        B > INT32_MAX / verify_chunks(V))
+        return PN_ERR_SHAPE;
+    if (B == 0)
+        return PN_OK;
+    if (!p || !u_sample || !tokens || !accepted || !workspace || (K > 0 && (!draft || !u_accept)))
+        return PN_ERR_NULL;
+    if (!aligned(p, size) || !aligned(q, size) || !aligned(draft, 4) || !aligned(n_draft, 4) ||
+        !aligned(u_accept, 4) || !aligned(u_sample, 4) || !aligned(tokens, 4) ||
+        !aligned(accepted, 4) || !aligned(workspace, 16))
+        return PN_ERR_ALIGN;
+    if (workspace_bytes < pn_verify_workspace_bytes(B, V))
+        return PN_ERR_WORKSPACE;
+    const int st = check_device();
+    if (st != PN_OK)
+        return st;
+    const VerifyArgs A{p, q, p_stride, q_stride, draft, n_draft, u_accept, u_sample, V, (int)K,
+                       (int)verify_chunks(V), tokens, accepted, (double2 *)workspace};
+    hipStream_t s = (hipStream_t)stream;
+    return type == PN_F32    ? launch_verify<PN_F32>(A, B, s)
+           : type == PN_BF16 ? launch_verify<PN_BF16>(A, B, s)
+                             : launch_verify<PN_F16>(A, B, s);
+}

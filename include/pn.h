@@ -51,7 +51,9 @@ enum {
                            NVFP4 codes not 8-byte aligned */
     PN_ERR_HIP = -6,    /* the HIP runtime reported an error (no device, launch failure) */
     PN_ERR_DEVICE = -7, /* the current device is not gfx950 */
-    PN_ERR_HADAMARD = -8 /* Hadamard slice size B is not a power of two in 2..16384 dividing K */
+    PN_ERR_HADAMARD = -8, /* Hadamard slice size B is not a power of two in 2..16384 dividing K */
+    PN_ERR_FORMAT = -9,   /* unknown cache format or element type */
+    PN_ERR_WORKSPACE = -10 /* the workspace is smaller than the call needs */
 };
 
 /* Maximum tokens per GEMV call. */
@@ -223,6 +225,135 @@ int pn_fp8row_dequantize_rows(const uint8_t *codes, const uint16_t *scales, int6
  * Deterministic. */
 int pn_gemv_fp8row(const uint8_t *codes, const uint16_t *scales, int64_t N, int64_t K,
                    const float *x, int64_t M, float *y, void *stream);
+
+/* ---- Microscaled key/value cache ---------------------------------------------------------------
+ * A paged cache of a layer's keys and values in microscaled floating point, quantised as it is
+ * written and decoded in registers as it is read. Per token and KV head, K and V are `dim` channels
+ * each (64, 128 or 256) in blocks of 32 channels; a block has one exponent byte b (E8M0) and 32
+ * codes of the format's element type:
+ *   PN_CACHE_MXFP8  E4M3FN codes, largest magnitude 448
+ *   PN_CACHE_MXFP4  E2M1 codes, largest magnitude 6, the even channel in the low nibble
+ * A channel stands for element(code) * 2^(b - 127), b = 255 for NaN whatever the code. Writing takes
+ * the smallest b >= 16 at which the block's largest magnitude is at most that of the element type
+ * times 2^(b - 127), and rounds x * 2^(127 - b), which is exact, once, to the nearest code, ties to
+ * the even one, the sign kept: every bit of the cache is fixed by these rules. (b >= 16 keeps every
+ * number a normal bfloat16 one.)
+ * A block with a NaN, an infinity or a magnitude of 2^127 or more has b = 255 and zero codes.
+ *
+ * Layout: [pages][heads][page / 32] records of 32 tokens, each of pn_cache_page_bytes / (heads *
+ * page / 32) bytes: K codes, V codes, K exponents, V exponents. In a record, with token 16a + i or
+ * 16a + 4g + t, channel chunk p of 64, block 2p + h:
+ *   K codes      MXFP8 [p][a][g][i][16 channels from 64p + 16g]
+ *                MXFP4 [p][g][i][a][16 channels from 64p + 16g]
+ *   V codes      MXFP8 [p][a][g][i][t][4 channels from 64p + 4i]
+ *                MXFP4 [p][g][i][a][t][4 channels from 64p + 4i]
+ *   K exponents  [h][i][p][a]        V exponents  [h][g][p][a][t]
+ * which is the order in which the matrix instructions of pn_attend take them: a wave reads each
+ * record as one contiguous run. data must be 16-byte aligned (PN_ERR_ALIGN). */
+enum { PN_CACHE_MXFP8 = 0, PN_CACHE_MXFP4 = 1 };
+/* Element types of plain tensors. */
+enum { PN_F32 = 0, PN_BF16 = 1, PN_F16 = 2 };
+
+typedef struct pn_cache {
+    int format;    /* PN_CACHE_MXFP8 or PN_CACHE_MXFP4 (else PN_ERR_FORMAT) */
+    int heads;     /* KV heads, at least 1 */
+    int dim;       /* channels a head: 64, 128 or 256 (else PN_ERR_SHAPE) */
+    int page;      /* tokens a page: a power of two in 32..1024 (else PN_ERR_SHAPE) */
+    int64_t pages; /* pages in data */
+    void *data;    /* pages * pn_cache_page_bytes bytes on the device */
+} pn_cache;
+
+/* Bytes of one page; 0 where the format, heads, dim or page is not one of the above. Host-only. */
+int64_t pn_cache_page_bytes(int format, int heads, int dim, int page);
+
+/* Quantises T tokens' keys and values into the cache. k and v are of `type`, the channels of a head
+ * contiguous, token t and head h at element t * token_stride + h * head_stride. slots int64[T] on
+ * the device: token t goes to place slots[t] % page of page slots[t] / page; a slot outside
+ * 0 .. pages * page - 1 (a padding token's -1) writes nothing. Slots of one call must differ. k and
+ * v need only their element's alignment (4 elements' alignment of bases and strides is faster). */
+int pn_cache_write(const pn_cache *cache, int type, const void *k, int64_t k_token_stride,
+                   int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                   int64_t v_head_stride, const int64_t *slots, int64_t T, void *stream);
+
+/* Reads T tokens back: k and v [T][heads][dim] of `type`, contiguous, aligned to 4 elements: the
+ * numbers above, exact in fp32 and bf16, rounded once to fp16. A slot outside the cache gives
+ * zeros. Slots may repeat. */
+int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t T, void *k, void *v,
+                  void *stream);
+
+/* ---- Attention over the cache --------------------------------------------------------------------
+ * B sequences of Q query tokens each (the tokens of one step: 1, or 1 + the drafted ones) attend to
+ * a prefix that all of them share and to their own tokens, both read from the cache (the own tokens
+ * include the step's, written before the call). Query token i of sequence b, head hq of Hq (KV head
+ * hq / (Hq / heads)):
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q.k_j),   lse = log sum_j w_j
+ * over every prefix token and the own tokens j <= lens[b] - nq + i, nq = q_lens[b] (Q where q_lens
+ * is NULL). A row that sees nothing, and every row i >= nq, is zeros with lse = -infinity.
+ * The prefix is computed for all sequences at once: its cache is read once per block of 64 rows
+ * (fp32 and fp16 queries: 32), not once per sequence.
+ *   q      [B][Q][Hq][dim] of `type` with strides in elements (channels contiguous)
+ *   table  int32[B][table_width] (row stride table_stride), the own pages of each sequence;
+ *          lens int32[B] own tokens, taken as 0..table_width * page
+ *   prefix_table int32[ceil(prefix_len / page)]
+ *   out    [B][Q][Hq][dim] of `type`, contiguous, 16-byte aligned; lse fp32[B][Q][Hq] or NULL
+ * A page number outside the cache is taken as the nearest one inside it: an unspecified value,
+ * no access out of bounds. Tokens past a sequence's length are not used, whatever lies there.
+ * Arithmetic: products on the matrix cores with fp32 sums; cache numbers enter exactly (bf16 holds
+ * them); running maxima and sums in fp32. bf16 q: the softmax weights are rounded to bf16 once
+ * (2^-8 relative at most) where they meet v. fp32 and fp16 q: q and the weights enter as two bf16
+ * parts each (2^-16 relative at most; an fp16 q exactly).
+ * Deterministic: a row's value depends on the call's shapes and its own data only.
+ * workspace: pn_attend_workspace_bytes of device memory (16-byte aligned), overwritten; it may be
+ * used by the next call on the same stream. */
+typedef struct pn_attend_args {
+    int type;                 /* PN_F32, PN_BF16 or PN_F16 */
+    int B, Q, Hq;             /* Hq a multiple of cache->heads (else PN_ERR_SHAPE) */
+    const void *q;
+    int64_t q_seq_stride, q_token_stride, q_head_stride;
+    float scale;              /* finite */
+    const int32_t *table;
+    int64_t table_stride;
+    int table_width;          /* pages a row of table has, 0 or more */
+    const int32_t *lens;
+    const int32_t *q_lens;    /* may be NULL */
+    const int32_t *prefix_table;
+    int64_t prefix_len;
+    void *out;
+    float *lse;               /* may be NULL */
+} pn_attend_args;
+
+/* Device bytes that pn_attend needs for these sizes (0 where none, or a size is invalid). Reads
+ * type, B, Q, Hq, table_width and prefix_len of a. */
+int64_t pn_attend_workspace_bytes(const pn_cache *cache, const pn_attend_args *a);
+
+int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *workspace,
+              int64_t workspace_bytes, void *stream);
+
+/* ---- Verification of drafted tokens --------------------------------------------------------------
+ * B sequences with K drafted tokens each (n = n_draft[b] of them, K where n_draft is NULL). p are the
+ * target's probabilities at the K + 1 positions, q the draft's at the K positions that the tokens
+ * were drawn from, or NULL where each draft is certain (q = 1 at the token, 0 elsewhere).
+ * Draft i is accepted iff every earlier one was and u_accept[b][i] * q_i(x_i) < p_i(x_i). After a
+ * accepted drafts comes one more token: the smallest t at which r_0 + .. + r_t > u_sample[b] * R,
+ * R the sum of all r; r = max(p_a - q_a, 0), where a < n and that has a positive sum, else r = p_a.
+ * With u uniform in [0, 1) the tokens are distributed as the target's.
+ * Every product, difference, sum and comparison is in 64 bits. A NaN or a negative probability
+ * counts as 0 in r and refuses its draft; a draft outside 0..V-1 is refused (and r = p_a where q is
+ * NULL). Where no t qualifies (rounding of the last sum, u >= 1) the token is the last t with
+ * r_t > 0, and -1 where r is zero everywhere.
+ *   p  row (b, i) at element (b * (K + 1) + i) * p_stride, q at (b * K + i) * q_stride, both of
+ *      `type`; draft int32[B][K]; u_accept fp32[B][K]; u_sample fp32[B]; n_draft int32[B] or NULL,
+ *      taken as 0..K
+ *   tokens int32[B][K + 1]: the accepted drafts, the token after them, then -1; accepted int32[B]
+ * 0 <= K <= PN_VERIFY_MAX_DRAFTS, 1 <= V < 2^30. Deterministic. The workspace is
+ * pn_verify_workspace_bytes of device memory (16-byte aligned), overwritten. */
+#define PN_VERIFY_MAX_DRAFTS 63
+int64_t pn_verify_workspace_bytes(int64_t B, int64_t V);
+
+int pn_verify(int type, const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+              const int32_t *draft, const int32_t *n_draft, const float *u_accept,
+              const float *u_sample, int64_t B, int64_t K, int64_t V, int32_t *tokens,
+              int32_t *accepted, void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
