@@ -5,8 +5,8 @@
 // maximum m, l = sum exp(s - m) and O = sum exp(s - m) v, rescaled when m grows; partial results of
 // disjoint token ranges join as m = max m_i, l = sum l_i e^(m_i - m), O likewise.
 //
-// A wave holds RT tiles of 16 query rows (a row is one query token and head of a KV head's group;
-// in the prefix the rows of all sequences stand in one list) and walks records of 32 tokens:
+// Tiles are 16 query rows (a row is one query token and head of a KV head's group; in the prefix the
+// rows of all sequences stand in one list) by records of 32 tokens:
 //   S^T = K Q^T  16x16x32 bf16 matrix instructions, tokens as rows: lane (i, g) = (lane % 16,
 //                lane / 16) takes 16-channel pieces of token i straight from the record (16 bytes a
 //                lane, a wave's load is one contiguous run), converted exactly to bf16 with the
@@ -17,14 +17,27 @@
 //                two converted tokens makes the pairs along the tokens that the instruction takes.
 //                A lane's results belong to row i again, so the rescaling by exp(m - m') is its own
 //                row's and needs no exchange; only m takes two lane swaps a record.
-// No LDS and no barrier until the end: the four waves of a workgroup take every fourth record of the
-// workgroup's token range and join their results through LDS. The range is one of `splits` of a
-// sequence (or of the prefix), and a second kernel joins those.
+// (The block-scaled 8-bit matrix instructions would take K's codes as they are, but align the 128
+// products of a sum to 13 bits below the largest: measured, 2^8 + 127 * 2^-6 gives 2^8.)
+//
+// Two kinds of workgroup, both of eight waves, two a SIMD: a single wave issues a vector instruction
+// every 7 clocks here, two together every 4.6.
+//   stream  few rows: memory bound. A wave has one tile of rows, q in LDS, and every (8 / tiles)-th
+//           record of the workgroup's token range, from memory straight to registers; at the end the
+//           waves of a row tile join through LDS.
+//   shared  the prefix under more than 64 rows: bound by conversions and the matrix instructions. All
+//           waves walk the same records, each with its own 16 to 64 rows. Converting a record once a
+//           wave would cost as much as its products, so it is converted once a workgroup: four waves
+//           take a chunk of 64 channels of K each, four of V, and put the operands into LDS, a stage
+//           ahead (two stages, one barrier a stage).
+// A workgroup's token range is one of `splits` of its sequence's (or the prefix's), and a second
+// kernel joins those.
 #pragma once
 
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pn_cache.h"
 
@@ -32,19 +45,40 @@ namespace pn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Division of numbers below 2^31 by a fixed d: n * mul >> shift with mul = floor(2^shift / d) + 1 and
+// shift = 31 + ceil(log2 d). (mul * d - 2^shift is at most d <= 2^(shift - 31), so n times it stays
+// below 2^shift: exact.) Two instructions for the twenty of a division, in code that runs once and
+// cold.
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+    FastDiv() = default;
+    explicit FastDiv(int d)
+    {
+        shift = 31;
+        while ((int64_t)1 << (shift - 31) < d)
+            shift++;
+        mul = (uint32_t)(((uint64_t)1 << shift) / (uint32_t)d + 1);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)((uint64_t)(uint32_t)n * mul >> shift); }
+};
+
 struct AttendArgs {
     CacheView c;
     int type, B, Q, Hq, G;  // G query heads a KV head
+    FastDiv by_G, by_Q, by_Hq;
     const void *q;
     int64_t q_seq, q_tok, q_head;
-    int q_vec;     // q can be loaded 16 bytes at a time
+    int q_vec;     // q can be loaded four elements at a time
     float scale;   // |scale| * log2(e), at least the least normal number
-    int neg;       // scale < 0: q is negated as it is loaded
+    float sign;    // -1 where scale < 0: q is negated as it is loaded
     const int32_t *table, *lens, *q_lens, *prefix_table;
     int64_t table_stride;
     int table_width, prefix_len;
     int prefix_splits, prefix_blocks;  // token ranges and row blocks of the prefix (0 without one)
     int own_splits, own_blocks;        // token ranges of a sequence and row blocks of a KV head
+    int shared_tiles;                  // row tiles of a wave in the prefix's shared workgroups, or 0
+    int prefix_tiles, own_tiles;       // row tiles of a stream workgroup
     int direct;                        // one range in all: write out, nothing to join
     float *part;                       // [range][row][D]
     float2 *part_ml;                   // [range][row]: maximum (log2 units) and sum
@@ -80,67 +114,53 @@ __device__ __forceinline__ int query_tokens(const AttendArgs &A, int b)
     return A.q_lens ? min(max(A.q_lens[b], 0), A.Q) : A.Q;
 }
 
-__device__ __forceinline__ float load_elem(int type, const void *p, int64_t at)
+// Four channels of an output, at a multiple of four.
+__device__ __forceinline__ void store4(int type, void *p, int64_t at, f32x4_t x)
 {
-    return type == PN_F32    ? reinterpret_cast<const float *>(p)[at]
-           : type == PN_BF16 ? (float)reinterpret_cast<const __bf16 *>(p)[at]
-                             : (float)reinterpret_cast<const _Float16 *>(p)[at];
-}
-
-__device__ __forceinline__ void store_elem(int type, void *p, int64_t at, float x)
-{
+    typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+    typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
     if (type == PN_F32)
-        reinterpret_cast<float *>(p)[at] = x;
+        *reinterpret_cast<f32x4_t *>(reinterpret_cast<float *>(p) + at) = x;
     else if (type == PN_BF16)
-        reinterpret_cast<__bf16 *>(p)[at] = (__bf16)x;
+        *reinterpret_cast<bf16x4_t *>(reinterpret_cast<__bf16 *>(p) + at) = __builtin_convertvector(x, bf16x4_t);
     else
-        reinterpret_cast<_Float16 *>(p)[at] = (_Float16)x;
+        *reinterpret_cast<f16x4_t *>(reinterpret_cast<_Float16 *>(p) + at) = __builtin_convertvector(x, f16x4_t);
 }
 
-// Eight channels of q as NT bf16 parts: the value rounded, then what that left. bf16 q has one part
-// (exact), fp16 two (exact: 11 bits), fp32 two (2^-16 relative at most).
-template <int NT>
-__device__ __forceinline__ void load_q8(const AttendArgs &A, int64_t at, bool live,
-                                        bf16x8_t (&part)[NT])
+// N pieces of eight channels of q, piece i at q + at + 64 (i / 2) + 8 (i % 2), as NT bf16 parts: the value
+// rounded, then what that left, and so on: bf16 q has one part, fp16 two, fp32 three, each exact (8, 16
+// and 24 bits). All loads are begun before the first is waited for.
+template <int NT, int N>
+__device__ __forceinline__ void load_q(const AttendArgs &A, int64_t at, bool live, bf16x8_t (&part)[N][NT])
 {
-    float x[8];
+    typedef typename Elem<NT == 1 ? PN_BF16 : NT == 2 ? PN_F16 : PN_F32>::type E;
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    const E *const p = reinterpret_cast<const E *>(A.q) + (live ? at : 0);
+    E4 x[N][2];
+    if (A.q_vec) {
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        x[j] = 0.0f;
-    if (live) {
-        if (A.q_vec && A.type == PN_F32) {
-            const f32x4_t *p = reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(A.q) + at);
-            const f32x4_t a = p[0], b = p[1];
+        for (int i = 0; i < N; i++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                x[j] = a[j];
-                x[4 + j] = b[j];
+            for (int j = 0; j < 2; j++)
+                x[i][j] = *reinterpret_cast<const E4 *>(p + 64 * (i / 2) + 8 * (i % 2) + 4 * j);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                x[i][j / 4][j % 4] = p[64 * (i / 2) + 8 * (i % 2) + j];
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float v = live ? (float)x[i][j / 4][j % 4] * A.sign : 0.0f;
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                part[i][t][j] = (__bf16)v;
+                v -= (float)part[i][t][j];
             }
-        } else if (A.q_vec && A.type == PN_BF16) {
-            const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(reinterpret_cast<const __bf16 *>(A.q) + at);
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                x[j] = (float)a[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                x[j] = load_elem(A.type, A.q, at + j);
         }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        float v = A.neg ? -x[j] : x[j];
-#pragma unroll
-        for (int t = 0; t < NT; t++) {
-            part[t][j] = (__bf16)v;
-            v -= (float)part[t][j];
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t dword(const uint4 &v, int i)
-{
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 __device__ __forceinline__ float exp_bits(uint32_t w) { return __builtin_bit_cast(float, w); }
@@ -162,14 +182,18 @@ __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// The larger of two numbers, the other where one is NaN, up to the largest finite one. (fmaxf would
+// first quiet each operand, an instruction apiece.)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, 0x1.fffffep127f); }
+
 __device__ __forceinline__ float over_groups_max(float v)
 {
     float a = v, b = v;
     swap32(a, b);
-    v = fmaxf(a, b);
+    v = larger(a, b);
     a = b = v;
     swap16(a, b);
-    return fmaxf(a, b);
+    return larger(a, b);
 }
 __device__ __forceinline__ float over_groups_sum(float v)
 {
@@ -181,186 +205,316 @@ __device__ __forceinline__ float over_groups_sum(float v)
     return a + b;
 }
 
-// A record's K (or V) half in a lane's registers.
-template <int FMT, int D>
-struct KReg {
-    static constexpr int N = (FMT == PN_CACHE_MXFP8 ? 2 : 1) * Rec<FMT, D>::NP;
-    uint4 w[N];
-    uint32_t e[2];  // byte 2p + a: the exponent of chunk p, half a (this lane's token and block)
-};
-template <int FMT, int D>
-struct VReg {
-    static constexpr int N = KReg<FMT, D>::N;
-    uint4 w[N];
-    uint32_t e[2 * Rec<FMT, D>::NP];  // word 2p + a: the exponents of this lane's four tokens
-};
-
-template <int FMT, int D>
-__device__ __forceinline__ void load_k(const uint8_t *rec, int lane, KReg<FMT, D> &k)
+// The scale operand from byte `byte` of an exponent word.
+__device__ __forceinline__ float scale_of(uint32_t w, int byte)
 {
-    constexpr int NP = Rec<FMT, D>::NP;
-#pragma unroll
-    for (int n = 0; n < KReg<FMT, D>::N; n++)
-        k.w[n] = *reinterpret_cast<const uint4 *>(rec + (n * 64 + lane) * 16);
-    const uint8_t *e = rec + Rec<FMT, D>::KE + ((lane >> 5) * 16 + (lane & 15)) * NP * 2;
-    if constexpr (NP == 1) {
-        k.e[0] = *reinterpret_cast<const uint16_t *>(e);
-    } else if constexpr (NP == 2) {
-        k.e[0] = *reinterpret_cast<const uint32_t *>(e);
-    } else {
-        const uint2 t = *reinterpret_cast<const uint2 *>(e);
-        k.e[0] = t.x;
-        k.e[1] = t.y;
-    }
+    return exp_bits(byte == 0 ? w << 23 : byte == 1 ? w << 15 : byte == 2 ? w << 7 : w >> 1);
 }
 
-template <int FMT, int D>
-__device__ __forceinline__ void load_v(const uint8_t *rec, int lane, VReg<FMT, D> &v)
+// An offset that is worked out where it is used: beside a uniform base it is one register of the load,
+// while the compiler would keep it as a 64-bit one over the whole loop.
+__device__ __forceinline__ uint32_t here(uint32_t offset)
 {
-    constexpr int NP = Rec<FMT, D>::NP;
-#pragma unroll
-    for (int n = 0; n < VReg<FMT, D>::N; n++)
-        v.w[n] = *reinterpret_cast<const uint4 *>(rec + Rec<FMT, D>::V + (n * 64 + lane) * 16);
-    const uint2 *e = reinterpret_cast<const uint2 *>(
-        rec + Rec<FMT, D>::VE + (((lane >> 3) & 1) * 4 + (lane >> 4)) * NP * 8);
-#pragma unroll
-    for (int p = 0; p < NP; p++) {
-        const uint2 t = e[p];
-        v.e[2 * p] = t.x;
-        v.e[2 * p + 1] = t.y;
-    }
+    asm volatile("" : "+v"(offset));
+    return offset;
 }
 
-// Eight channels (piece half J) of chunk p of this lane's token of half a.
-template <int FMT, int D>
-__device__ __forceinline__ bf16x8_t k_frag(const KReg<FMT, D> &k, int p, int a, int j)
+// A lane's part of one 64-channel chunk of a record's K or V, tokens of half a: 16 codes. K: 16 channels
+// of a token; V: four channels of four tokens.
+template <int FMT>
+struct Half {
+    static constexpr int N = FMT == PN_CACHE_MXFP8 ? 4 : 2;
+    uint32_t d[N];
+};
+template <int FMT>
+struct Chunk {
+    Half<FMT> h[2];
+};
+// Chunk p of the codes at `codes`: 16 bytes a lane and load, a wave's load one contiguous KB (with 8-bit
+// codes one a half).
+template <int FMT>
+__device__ __forceinline__ void load_chunk(const uint8_t *codes, int p, int lane, Chunk<FMT> &c)
 {
-    const int byte = 2 * p + a;
-    const uint32_t w = k.e[byte >> 2];
-    const int b = byte & 3;
-    const float s = exp_bits(b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1);
-    uint32_t r[4];
+    const uint32_t at = here(lane * 16);
     if constexpr (FMT == PN_CACHE_MXFP8) {
-        const uint32_t lo = dword(k.w[2 * p + a], 2 * j), hi = dword(k.w[2 * p + a], 2 * j + 1);
-        r[0] = pair<FMT, 0>(lo, s);
-        r[1] = pair<FMT, 1>(lo, s);
-        r[2] = pair<FMT, 0>(hi, s);
-        r[3] = pair<FMT, 1>(hi, s);
+#pragma unroll
+        for (int a = 0; a < 2; a++) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(codes + (p * 2 + a) * 1024 + at);
+            c.h[a] = Half<FMT>{{w.x, w.y, w.z, w.w}};
+        }
     } else {
-        const uint32_t lo = dword(k.w[p], 2 * a + j);
-        r[0] = pair<FMT, 0>(lo, s);
-        r[1] = pair<FMT, 1>(lo, s);
-        r[2] = pair<FMT, 2>(lo, s);
-        r[3] = pair<FMT, 3>(lo, s);
+        const uint4 w = *reinterpret_cast<const uint4 *>(codes + p * 1024 + at);
+        c.h[0] = Half<FMT>{{w.x, w.y}};
+        c.h[1] = Half<FMT>{{w.z, w.w}};
     }
-    return __builtin_bit_cast(bf16x8_t, make_uint4(r[0], r[1], r[2], r[3]));
+}
+// Half a of it alone.
+template <int FMT>
+__device__ __forceinline__ void load_half(const uint8_t *codes, int p, int a, int lane, Half<FMT> &h)
+{
+    if constexpr (FMT == PN_CACHE_MXFP8) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(codes + (p * 2 + a) * 1024 + here(lane * 16));
+        h = Half<FMT>{{w.x, w.y, w.z, w.w}};
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(codes + p * 1024 + a * 8 + here(lane * 16));
+        h = Half<FMT>{{w.x, w.y}};
+    }
+}
+// Where this lane's exponents are in a record: K's 2 NP bytes [p][a], V's 2 NP words [p][a].
+template <int FMT, int D>
+__device__ __forceinline__ uint32_t k_exps(int lane)
+{
+    return here(((lane >> 5) * 16 + (lane & 15)) * Rec<FMT, D>::NP * 2);
+}
+template <int FMT, int D>
+__device__ __forceinline__ uint32_t v_exps(int lane)
+{
+    return here((((lane >> 3) & 1) * 4 + (lane >> 4)) * Rec<FMT, D>::NP * 8);
 }
 
-// Chunk p of V as four operands: operand n holds channel 64p + 4i + n of this lane's eight tokens.
-template <int FMT, int D>
-__device__ __forceinline__ void v_frags(const VReg<FMT, D> &v, int p, bf16x8_t (&f)[4])
+// K operand: channels 8j .. 8j + 7 of the lane's 16, scale s.
+template <int FMT>
+__device__ __forceinline__ bf16x8_t k_frag(const Half<FMT> &h, int j, float s)
 {
-    uint32_t r[4][4];
+    uint4 r;
+    if constexpr (FMT == PN_CACHE_MXFP8)
+        r = make_uint4(pair<FMT, 0>(h.d[2 * j], s), pair<FMT, 1>(h.d[2 * j], s),
+                       pair<FMT, 0>(h.d[2 * j + 1], s), pair<FMT, 1>(h.d[2 * j + 1], s));
+    else
+        r = make_uint4(pair<FMT, 0>(h.d[j], s), pair<FMT, 1>(h.d[j], s), pair<FMT, 2>(h.d[j], s),
+                       pair<FMT, 3>(h.d[j], s));
+    return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// V operands of a chunk p: operand n holds channel 64p + 4i + n of the lane's eight tokens; here the
+// four of a half, e their exponents.
+template <int FMT>
+__device__ __forceinline__ void v_half(const Half<FMT> &h, uint32_t e, uint2 (&f)[4])
+{
+    uint32_t c01[4], c23[4];
 #pragma unroll
-    for (int a = 0; a < 2; a++) {
-        const uint32_t w = v.e[2 * p + a];
-        const float s[4] = {exp_bits(w << 23), exp_bits(w << 15), exp_bits(w << 7), exp_bits(w >> 1)};
-        uint32_t c01[4], c23[4];
+    for (int t = 0; t < 4; t++) {
+        const float s = scale_of(e, t);
         if constexpr (FMT == PN_CACHE_MXFP8) {
-#pragma unroll
-            for (int t = 0; t < 4; t++) {
-                c01[t] = pair<FMT, 0>(dword(v.w[2 * p + a], t), s[t]);
-                c23[t] = pair<FMT, 1>(dword(v.w[2 * p + a], t), s[t]);
-            }
+            c01[t] = pair<FMT, 0>(h.d[t], s);
+            c23[t] = pair<FMT, 1>(h.d[t], s);
+        } else if (t & 1) {
+            c01[t] = pair<FMT, 2>(h.d[t / 2], s);
+            c23[t] = pair<FMT, 3>(h.d[t / 2], s);
         } else {
-#pragma unroll
-            for (int t = 0; t < 4; t += 2) {
-                const uint32_t d = dword(v.w[p], 2 * a + t / 2);
-                c01[t] = pair<FMT, 0>(d, s[t]);
-                c23[t] = pair<FMT, 1>(d, s[t]);
-                c01[t + 1] = pair<FMT, 2>(d, s[t + 1]);
-                c23[t + 1] = pair<FMT, 3>(d, s[t + 1]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-            r[0][2 * a + t] = __builtin_amdgcn_perm(c01[2 * t + 1], c01[2 * t], 0x05040100);
-            r[1][2 * a + t] = __builtin_amdgcn_perm(c01[2 * t + 1], c01[2 * t], 0x07060302);
-            r[2][2 * a + t] = __builtin_amdgcn_perm(c23[2 * t + 1], c23[2 * t], 0x05040100);
-            r[3][2 * a + t] = __builtin_amdgcn_perm(c23[2 * t + 1], c23[2 * t], 0x07060302);
+            c01[t] = pair<FMT, 0>(h.d[t / 2], s);
+            c23[t] = pair<FMT, 1>(h.d[t / 2], s);
         }
     }
+    constexpr uint32_t lo = 0x05040100, hi = 0x07060302;
+    f[0] = make_uint2(__builtin_amdgcn_perm(c01[1], c01[0], lo), __builtin_amdgcn_perm(c01[3], c01[2], lo));
+    f[1] = make_uint2(__builtin_amdgcn_perm(c01[1], c01[0], hi), __builtin_amdgcn_perm(c01[3], c01[2], hi));
+    f[2] = make_uint2(__builtin_amdgcn_perm(c23[1], c23[0], lo), __builtin_amdgcn_perm(c23[3], c23[2], lo));
+    f[3] = make_uint2(__builtin_amdgcn_perm(c23[1], c23[0], hi), __builtin_amdgcn_perm(c23[3], c23[2], hi));
+}
+template <int FMT>
+__device__ __forceinline__ void v_frags(const Chunk<FMT> &v, const uint32_t (&e)[2], bf16x8_t (&f)[4])
+{
+    uint2 r[2][4];
+    v_half<FMT>(v.h[0], e[0], r[0]);
+    v_half<FMT>(v.h[1], e[1], r[1]);
 #pragma unroll
     for (int n = 0; n < 4; n++)
-        f[n] = __builtin_bit_cast(bf16x8_t, make_uint4(r[n][0], r[n][1], r[n][2], r[n][3]));
+        f[n] = __builtin_bit_cast(bf16x8_t, make_uint4(r[0][n].x, r[0][n].y, r[1][n].x, r[1][n].y));
 }
 
-// Token (a, t) of this lane's eight, chunk p: zeros.
-template <int FMT, int D>
-__device__ __forceinline__ void v_clear(VReg<FMT, D> &v, int p, int a, int t)
+// Token t of the four in a half of V: zeros.
+template <int FMT>
+__device__ __forceinline__ void v_clear(Half<FMT> &h, uint32_t &e, int t)
 {
-    uint4 &w = v.w[FMT == PN_CACHE_MXFP8 ? 2 * p + a : p];
-    const int d = FMT == PN_CACHE_MXFP8 ? t : 2 * a + t / 2;
-    const uint32_t keep = FMT == PN_CACHE_MXFP8 ? 0u : t & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-    if (d == 0)
-        w.x &= keep;
-    else if (d == 1)
-        w.y &= keep;
-    else if (d == 2)
-        w.z &= keep;
+    if constexpr (FMT == PN_CACHE_MXFP8)
+        h.d[t] = 0;
     else
-        w.w &= keep;
-    v.e[2 * p + a] &= ~(255u << (8 * t));
+        h.d[t / 2] &= t & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    e &= ~(255u << (8 * t));
 }
 
 // NaN blocks in a record that some rows see only in part: a weight of zero must not meet them. They
 // are taken out of V, and what they do to the rows that see them is done here: a product of "is NaN"
 // with "is seen" counts, for each row and channel, the NaNs that belong to its sum.
-template <int FMT, int D, int RT>
-__device__ __forceinline__ void v_nan_apart(VReg<FMT, D> &v, const f32x4_t (&s)[RT][2],
-                                            f32x4_t (&O)[RT][Rec<FMT, D>::NP][4])
+template <int FMT>
+__device__ __forceinline__ void v_nan_apart(Chunk<FMT> &v, uint32_t (&e)[2], const f32x4_t (&s)[2],
+                                            f32x4_t (&O)[4])
 {
-    constexpr int NP = Rec<FMT, D>::NP;
+    bf16x8_t bad, seen;
 #pragma unroll
-    for (int p = 0; p < NP; p++) {
-        bf16x8_t bad;
+    for (int a = 0; a < 2; a++)
 #pragma unroll
-        for (int a = 0; a < 2; a++)
+        for (int t = 0; t < 4; t++) {
+            const bool nan = ((e[a] >> (8 * t)) & 255u) == 255u;
+            bad[4 * a + t] = (__bf16)(nan ? 1.0f : 0.0f);
+            seen[4 * a + t] = (__bf16)(s[a][t] == -INFINITY ? 0.0f : 1.0f);
+            if (nan)
+                v_clear<FMT>(v.h[a], e[a], t);
+        }
+    const f32x4_t count = mfma(bad, seen, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-            for (int t = 0; t < 4; t++) {
-                const bool nan = ((v.e[2 * p + a] >> (8 * t)) & 255u) == 255u;
-                bad[4 * a + t] = (__bf16)(nan ? 1.0f : 0.0f);
-                if (nan)
-                    v_clear<FMT, D>(v, p, a, t);
-            }
+    for (int n = 0; n < 4; n++)
 #pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            bf16x8_t seen;
+        for (int r = 0; r < 4; r++)
+            O[n][r] = count[r] > 0.0f ? __builtin_nanf("") : O[n][r];
+}
+
+// A row's reference m of the weights 2^(s - m) (near its running maximum; all four lanes of a row have
+// the same), the lane's own part l of their sum, and O. `base` is -m: infinity before any token.
+template <int NP>
+struct State {
+    float base, l;
+    f32x4_t O[NP][4];
+    __device__ __forceinline__ void clear()
+    {
+        base = INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int p = 0; p < NP; p++)
+#pragma unroll
+            for (int n = 0; n < 4; n++)
+                O[p][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+};
+
+// Scores of NR records to weights for RT tiles, as NT bf16 parts in the order of the V operand's tokens.
+// The weights are taken against the reference as it is; only where a lane's sum of them passes 2^12
+// (or is NaN: no reference yet) are the maximum found, the reference moved to it and the weights taken
+// again. Weights up to 2^12 lose nothing in fp32 and bf16, and most records need neither the maximum,
+// which is as many instructions as the rest, nor a rescaling.
+template <int NT, int NP, int NR, int RT>
+__device__ __forceinline__ void weigh(const f32x4_t (&s)[RT][NR][2], float scale, State<NP> (&st)[RT],
+                                      bf16x8_t (&w)[RT][NR][NT])
+{
+    const auto weights = [&](int rt, float (&x)[NR][8]) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NR; c++) {
 #pragma unroll
             for (int a = 0; a < 2; a++)
 #pragma unroll
                 for (int r = 0; r < 4; r++)
-                    seen[4 * a + r] = (__bf16)(s[rt][a][r] == -INFINITY ? 0.0f : 1.0f);
-            const f32x4_t count = mfma(bad, seen, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                    x[c][4 * a + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][c][a][r], scale, st[rt].base));
+            const float part = ((x[c][0] + x[c][1]) + (x[c][2] + x[c][3])) + ((x[c][4] + x[c][5]) + (x[c][6] + x[c][7]));
+            sum = c ? sum + part : part;
+        }
+        return sum;
+    };
+    const auto put = [&](int rt, float (&x)[NR][8]) {
 #pragma unroll
-            for (int n = 0; n < 4; n++)
+        for (int c = 0; c < NR; c++)
 #pragma unroll
-                for (int r = 0; r < 4; r++)
-                    O[rt][p][n][r] = count[r] > 0.0f ? __builtin_nanf("") : O[rt][p][n][r];
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int r = 0; r < 8; r++) {
+                    w[rt][c][n][r] = (__bf16)x[c][r];
+                    if (n + 1 < NT)
+                        x[c][r] -= (float)w[rt][c][n][r];
+                }
+    };
+    float sum[RT];
+    bool over = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        float x[NR][8];
+        sum[rt] = weights(rt, x);
+        over |= !(sum[rt] <= 0x1p12f);
+        put(rt, x);
+    }
+    if (__any(over)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NR; c++)
+#pragma unroll
+                for (int a = 0; a < 2; a++)
+                    top = larger(larger(top, larger(s[rt][c][a][0], s[rt][c][a][1])),
+                                 larger(s[rt][c][a][2], s[rt][c][a][3]));
+            top = larger(over_groups_max(top) * scale, -st[rt].base);
+            // (2^(m - top) of no reference at all: there is nothing to rescale, or it is NaN and stays so)
+            const float f = st[rt].base == INFINITY ? 0.0f : __builtin_amdgcn_exp2f(-st[rt].base - top);
+            st[rt].l *= f;
+#pragma unroll
+            for (int p = 0; p < NP; p++)
+#pragma unroll
+                for (int n = 0; n < 4; n++)
+                    st[rt].O[p][n] *= f;
+            // no token seen: any finite reference gives weights of zero
+            const bool none = top == -INFINITY;
+            st[rt].base = none ? 0.0f : -top;
+            float x[NR][8];
+            sum[rt] = weights(rt, x);
+            put(rt, x);
+            if (none)
+                st[rt].base = INFINITY;
         }
     }
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++)
+        st[rt].l += sum[rt];
 }
 
-// One workgroup's share: rows [row0, row0 + 16 RT) of KV head h over range `split` of a sequence's
-// own tokens (OWN) or of the prefix.
-template <int FMT, int D, int NT, int RT, bool OWN>
-__device__ __forceinline__ void attend_part(const AttendArgs &A, int split, int b0, int h, int row0,
-                                            float *lds)
+// Where a row is: its sequence, query token, place in q and in out.
+struct Row {
+    int b, i;
+    int64_t q, out;
+};
+template <bool OWN>
+__device__ __forceinline__ Row row_of(const AttendArgs &A, int b0, int h, int row)
+{
+    Row r;
+    const int qt = A.by_G.of(row);  // query token, counted over all sequences in the prefix
+    const int hq = h * A.G + row - qt * A.G;
+    r.b = OWN ? b0 : A.by_Q.of(qt);
+    r.i = OWN ? qt : qt - r.b * A.Q;
+    r.q = r.b * A.q_seq + r.i * A.q_tok + hq * A.q_head;
+    r.out = ((int64_t)r.b * A.Q + r.i) * A.Hq + hq;
+    return r;
+}
+
+// A number that every lane reads and no one writes while the kernel runs, by a scalar load: a vector
+// load would be waited for behind the cache's loads in flight.
+__device__ __forceinline__ int32_t load_uniform(const int32_t *p)
+{
+    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uintptr_t>(p));
+}
+
+// Records of KV head h of a sequence's own tokens or of the prefix.
+template <int FMT, int D>
+struct Records {
+    const uint8_t *head;  // the head's first record in page 0
+    const int32_t *table;
+    int64_t page_bytes;
+    int shift, pages;  // log2 of the records a page has; pages of the cache
+    __device__ __forceinline__ Records(const AttendArgs &A, const int32_t *table, int h)
+        : table(table), shift(A.c.page_shift - 5), pages((int)A.c.pages)
+    {
+        const int64_t bytes = (int64_t)Rec<FMT, D>::BYTES << shift;  // of one head
+        head = A.c.data + h * bytes;
+        page_bytes = A.c.heads * bytes;
+    }
+    __device__ __forceinline__ int page(int t) const { return load_uniform(table + (t >> shift)); }
+    // a page number outside the cache is taken as the nearest inside
+    __device__ __forceinline__ const uint8_t *at(int page, int t) const
+    {
+        return head + min(max(page, 0), pages - 1) * page_bytes + (t & ((1 << shift) - 1)) * Rec<FMT, D>::BYTES;
+    }
+};
+
+constexpr int kWaves = 8;
+
+// A stream workgroup: rows [row0, row0 + 16 tiles) of KV head h over range `split` of a sequence's own
+// tokens (OWN) or of the prefix. Wave w has row tile w % tiles and every (8 / tiles)-th record.
+template <int FMT, int D, int NT, bool OWN>
+__device__ __forceinline__ void attend_stream(const AttendArgs &A, int split, int b0, int h, int row0, int tiles,
+                                              uint4 *lds)
 {
     constexpr int NP = Rec<FMT, D>::NP;
-    typedef Rec<FMT, D> R;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
+    const int tile = wave & (tiles - 1), streams = kWaves / tiles, stream = wave / tiles;
 
     const int nrows = (OWN ? 1 : A.B) * A.Q * A.G;
     const int tokens = OWN ? own_tokens(A, b0) : A.prefix_len;
@@ -370,85 +524,92 @@ __device__ __forceinline__ void attend_part(const AttendArgs &A, int split, int 
     if (range.begin >= range.end && !A.direct)
         return;
 
-    // this lane's rows: where they are in q and out, and up to which token they see
-    int limit[RT];
-    bf16x8_t q[RT][NP][2][NT];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        const int row = row0 + 16 * rt + i16;
-        const bool live = row < nrows;
-        const int r = live ? row : 0;
-        const int qt = r / A.G;  // query token, counted over all sequences in the prefix
-        const int b = OWN ? b0 : qt / A.Q, i = OWN ? qt : qt - b * A.Q;
-        limit[rt] = !OWN ? tokens : i < nq ? min(tokens, tokens - nq + i + 1) : 0;
-        const int64_t at = b * A.q_seq + i * A.q_tok + (h * A.G + r - qt * A.G) * A.q_head;
+    const Records<FMT, D> recs(A, OWN ? A.table + b0 * A.table_stride : A.prefix_table, h);
+    Chunk<FMT> kc[NP], vc[NP];
+    uint32_t ke[2], ve[NP][2];
+    auto load_k = [&](const uint8_t *rec) {
 #pragma unroll
         for (int p = 0; p < NP; p++)
-#pragma unroll
-            for (int j = 0; j < 2; j++)
-                load_q8<NT>(A, at + 64 * p + 16 * g + 8 * j, live, q[rt][p][j]);
-    }
-
-    f32x4_t O[RT][NP][4];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        m[rt] = -INFINITY;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int p = 0; p < NP; p++)
-#pragma unroll
-            for (int n = 0; n < 4; n++)
-                O[rt][p][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    const int32_t *table = OWN ? A.table + b0 * A.table_stride : A.prefix_table;
-    const int tshift = A.c.page_shift - 5;  // log2 of the records a page has
-    auto page_of = [&](int t) {
-        const int64_t page = table[t >> tshift];
-        return page < 0 ? (int64_t)0 : min(page, A.c.pages - 1);
+            load_chunk<FMT>(rec, p, lane, kc[p]);
+        const uint8_t *e = rec + Rec<FMT, D>::KE + k_exps<FMT, D>(lane);
+        if constexpr (NP == 1)
+            ke[0] = *reinterpret_cast<const uint16_t *>(e);
+        else
+            ke[0] = *reinterpret_cast<const uint32_t *>(e);
+        if constexpr (NP == 4)
+            ke[1] = *reinterpret_cast<const uint32_t *>(e + 4);
     };
-    auto record = [&](int64_t page, int t) -> const uint8_t * {
-        return A.c.data + (((page * A.c.heads + h) << tshift) + (t & ((1 << tshift) - 1))) * R::BYTES;
+    auto load_v = [&](const uint8_t *rec) {
+        const uint2 *e = reinterpret_cast<const uint2 *>(rec + Rec<FMT, D>::VE + v_exps<FMT, D>(lane));
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            load_chunk<FMT>(rec + Rec<FMT, D>::V, p, lane, vc[p]);
+            const uint2 t = e[p];
+            ve[p][0] = t.x;
+            ve[p][1] = t.y;
+        }
     };
-
-    KReg<FMT, D> kr;
-    VReg<FMT, D> vr;
-    int t = range.begin + wave;
-    int64_t next_page = 0;
+    int t = range.begin + stream;
+    int next_page = 0;
     if (t < range.end) {
-        const uint8_t *rec = record(page_of(t), t);
-        load_k<FMT, D>(rec, lane, kr);
-        load_v<FMT, D>(rec, lane, vr);
-        if (t + 4 < range.end)
-            next_page = page_of(t + 4);
+        const uint8_t *rec = recs.at(recs.page(t), t);
+        load_k(rec);
+        load_v(rec);
+        if (t + streams < range.end)
+            next_page = recs.page(t + streams);
     }
-    for (; t < range.end; t += 4) {
-        const bool more = t + 4 < range.end;
-        const uint8_t *next = record(next_page, t + 4);
 
-        // scores of 2 x 16 tokens
-        f32x4_t s[RT][2];
+    // q operands to LDS: [tile][p][j][part][lane]
+    for (int u = wave; u < tiles * NP; u += kWaves) {
+        const int row = row0 + 16 * (u / NP) + i16;
+        const Row r = row_of<OWN>(A, b0, h, row < nrows ? row : 0);
+        bf16x8_t part[2][NT];
+        load_q<NT, 2>(A, r.q + 64 * (u % NP) + 16 * g, row < nrows, part);
 #pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-            s[rt][0] = s[rt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < 2 * NT; n++)
+            lds[(u * 2 * NT + n) * 64 + lane] = __builtin_bit_cast(uint4, part[n / NT][n % NT]);
+    }
+    int limit = 0;  // this lane's row sees the tokens below
+    {
+        const int row = row0 + 16 * tile + i16;
+        const Row r = row_of<OWN>(A, b0, h, row < nrows ? row : 0);
+        limit = !OWN ? tokens : r.i < nq ? min(tokens, tokens - nq + r.i + 1) : 0;
+    }
+    __syncthreads();
+    const uint4 *const q = lds + tile * NP * 2 * NT * 64 + lane;
+
+    State<NP> state[1];
+    State<NP> &st = state[0];
+    st.clear();
+    for (; t < range.end; t += streams) {
+        const bool more = t + streams < range.end;
+        const uint8_t *next = recs.at(next_page, t + streams);
+        // q stays in LDS: read before the loop, its operands would take the registers of the loads
+        // in flight
+        int fresh = 0;
+        asm volatile("" : "+v"(fresh));
+
+        f32x4_t s[1][1][2] = {{{f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}}}};
 #pragma unroll
         for (int p = 0; p < NP; p++)
 #pragma unroll
-            for (int a = 0; a < 2; a++)
+            for (int j = 0; j < 2; j++) {
+                bf16x8_t qf[NT];
 #pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const bf16x8_t kf = k_frag<FMT, D>(kr, p, a, j);
+                for (int n = 0; n < NT; n++)
+                    qf[n] = __builtin_bit_cast(bf16x8_t, q[((p * 2 + j) * NT + n) * 64 + fresh]);
 #pragma unroll
-                    for (int rt = 0; rt < RT; rt++)
+                for (int a = 0; a < 2; a++) {
+                    const bf16x8_t kf = k_frag<FMT>(kc[p].h[a], j, scale_of(ke[p >> 1], 2 * (p & 1) + a));
 #pragma unroll
-                        for (int n = 0; n < NT; n++)
-                            s[rt][a] = mfma(kf, q[rt][p][j][n], s[rt][a]);
+                    for (int n = 0; n < NT; n++)
+                        s[0][0][a] = mfma(kf, qf[n], s[0][0][a]);
                 }
+            }
         if (more) {
-            load_k<FMT, D>(next, lane, kr);
-            if (t + 8 < range.end)
-                next_page = page_of(t + 8);
+            load_k(next);
+            if (t + 2 * streams < range.end)
+                next_page = recs.page(t + 2 * streams);
         }
 
         // the record holds tokens that some row does not see: those count nothing, and what lies
@@ -460,282 +621,551 @@ __device__ __forceinline__ void attend_part(const AttendArgs &A, int split, int 
             for (int a = 0; a < 2; a++)
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-#pragma unroll
-                    for (int rt = 0; rt < RT; rt++)
-                        if (first + 16 * a + r >= limit[rt])
-                            s[rt][a][r] = -INFINITY;
+                    if (first + 16 * a + r >= limit)
+                        s[0][0][a][r] = -INFINITY;
                     if (first + 16 * a + r >= tokens) {
 #pragma unroll
-                        for (int p = 0; p < NP; p++) {
-                            v_clear<FMT, D>(vr, p, a, r);
-                        }
+                        for (int p = 0; p < NP; p++)
+                            v_clear<FMT>(vc[p].h[a], ve[p][a], r);
                     }
                 }
             if (OWN) {  // a NaN block of a token that only some rows see
                 bool any = false;
 #pragma unroll
-                for (int p = 0; p < 2 * NP; p++)
+                for (int p = 0; p < NP; p++)
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        any |= ((vr.e[p] >> (8 * r)) & 255u) == 255u;
+                    for (int r = 0; r < 8; r++)
+                        any |= ((ve[p][r >> 2] >> (8 * (r & 3))) & 255u) == 255u;
                 nan_hidden = __any(any);
             }
         }
 
-        uint32_t pw[RT][NT][4];
+        bf16x8_t w[1][1][NT];
+        weigh<NT, NP, 1, 1>(s, A.scale, state, w);
+        if (nan_hidden) {
 #pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            float top = fmaxf(fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3])),
-                              fmaxf(fmaxf(s[rt][1][0], s[rt][1][1]), fmaxf(s[rt][1][2], s[rt][1][3])));
-            top = over_groups_max(top) * A.scale;
-            // the maximum may lag by 2^8 of growth: weights up to 256 lose nothing, and most
-            // records need no rescaling
-            if (__any(top > m[rt] + 8.0f)) {
-                const float now = fmaxf(m[rt], top);
-                const float f = now == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[rt] - now);
-                m[rt] = now;
-                l[rt] *= f;
-#pragma unroll
-                for (int p = 0; p < NP; p++)
-#pragma unroll
-                    for (int n = 0; n < 4; n++)
-                        O[rt][p][n] *= f;
-            }
-            const float base = m[rt] == -INFINITY ? 0.0f : -m[rt];
-            float w[8];
-#pragma unroll
-            for (int a = 0; a < 2; a++)
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-                    w[4 * a + r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][a][r], A.scale, base));
-            l[rt] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const bf16x2_t v = {(__bf16)w[2 * r], (__bf16)w[2 * r + 1]};
-                    pw[rt][n][r] = __builtin_bit_cast(uint32_t, v);
-                    if (n + 1 < NT) {
-                        w[2 * r] -= (float)v.x;
-                        w[2 * r + 1] -= (float)v.y;
-                    }
-                }
+            for (int p = 0; p < NP; p++)
+                v_nan_apart<FMT>(vc[p], ve[p], s[0][0], st.O[p]);
         }
-
-        if (nan_hidden)
-            v_nan_apart<FMT, D, RT>(vr, s, O);
 #pragma unroll
         for (int p = 0; p < NP; p++) {
             bf16x8_t vf[4];
-            v_frags<FMT, D>(vr, p, vf);
+            v_frags<FMT>(vc[p], ve[p], vf);
 #pragma unroll
             for (int n = 0; n < 4; n++)
+#pragma unroll
+                for (int e = 0; e < NT; e++)
+                    st.O[p][n] = mfma(vf[n], w[0][0][e], st.O[p][n]);
+        }
+        if (more)
+            load_v(next);
+    }
+
+    // join the waves of each row tile: O of all waves in LDS, scaled to the tile's common reference,
+    // and each wave's part of the sum
+    constexpr int PAD = D + 4;
+    float *const buf = reinterpret_cast<float *>(lds);  // [wave][row][PAD]
+    float *const ms = buf + kWaves * 16 * PAD;          // [wave][row] references, then parts of the sum
+    float *const ls = ms + kWaves * 16;
+    const float lsum = over_groups_sum(st.l);
+    __syncthreads();
+    if (g == 0)
+        ms[wave * 16 + i16] = -st.base;
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+        const float m = ms[w * 16 + i16];
+        top = (w & (tiles - 1)) == tile ? fmaxf(top, m) : top;
+    }
+    // l = 0 only where a wave saw no token (l is NaN where its scores are)
+    const float f = lsum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(-st.base - top);
+#pragma unroll
+    for (int p = 0; p < NP; p++)
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+            *reinterpret_cast<f32x4_t *>(buf + (wave * 16 + i16) * PAD + 64 * p + 16 * g + 4 * r) =
+                f * f32x4_t{st.O[p][0][r], st.O[p][1][r], st.O[p][2][r], st.O[p][3][r]};
+    if (g == 0)
+        ls[wave * 16 + i16] = f * lsum;
+    __syncthreads();
+    const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
+    const int64_t slot = (OWN ? A.prefix_splits : 0) + split;
+    const auto join = [&](auto tiles_) {
+        constexpr int TILES = decltype(tiles_)::value;
+#pragma unroll
+        for (int u0 = 0; u0 < TILES * 16 * (D / 4); u0 += kWaves * 64) {
+            const int u = u0 + threadIdx.x;
+            const int cg = u % (D / 4), jr = u / (D / 4) % 16, ti = u / (D / 4) / 16;
+            const int row = row0 + 16 * ti + jr;
+            if (row >= nrows)
+                continue;
+            f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+            float sum = 0.0f, most = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWaves; w += TILES) {
+                v += *reinterpret_cast<const f32x4_t *>(buf + ((w + ti) * 16 + jr) * PAD + 4 * cg);
+                sum += ls[(w + ti) * 16 + jr];
+                most = fmaxf(most, ms[(w + ti) * 16 + jr]);
+            }
+            const Row r = row_of<OWN>(A, b0, h, row);
+            const int64_t at = r.out * D + 4 * cg;
+            if (A.direct) {
+                const bool none = sum == 0.0f || r.i >= nq;  // sees nothing, or not a query token
+                store4(A.type, A.out, at, none ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : v * (1.0f / sum));
+                if (cg == 0 && A.lse)
+                    A.lse[r.out] = none ? -INFINITY : (most + __builtin_amdgcn_logf(sum)) * kLn2;
+            } else {
+                *reinterpret_cast<f32x4_t *>(A.part + slot * rows * D + at) = v;
+                if (cg == 0)
+                    A.part_ml[slot * rows + r.out] = make_float2(most, sum);
+            }
+        }
+    };
+    if (tiles == 1)
+        join(std::integral_constant<int, 1>());
+    else if (tiles == 2)
+        join(std::integral_constant<int, 2>());
+    else
+        join(std::integral_constant<int, 4>());
+}
+
+// Rows a wave of a shared workgroup can hold at most, in tiles of 16, and the records of a stage: what
+// 256 registers take beside the operands in flight (a tile's O takes D / 4, its q D / 8 a part, its
+// scores 8 a record, its weights 4 a record and part).
+constexpr int shared_tiles(int D, int NT)
+{
+    return D == 256 ? (NT == 1 ? 2 : 1) : D == 128 ? (NT == 3 ? 1 : 2) : NT == 1 ? 3 : 2;
+}
+constexpr int stage_records(int D) { return D == 256 ? 1 : 2; }
+
+// Operands read from LDS AHEAD uses early: left to itself the compiler reads two, waits for both and
+// starts over, and an LDS read under load takes as long as several uses. begin() starts the first
+// reads, run() calls use(i, operand i) for the N operands at `from` (one every 64 uint4).
+template <int AHEAD>
+struct ReadAhead {
+    uint4 f[AHEAD];
+    __device__ __forceinline__ void begin(const uint4 *from)
+    {
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++)
+            f[i] = from[i * 64];
+    }
+    template <int N, typename F>
+    __device__ __forceinline__ void run(const uint4 *from, F use)
+    {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            use(i, __builtin_bit_cast(bf16x8_t, f[i % AHEAD]));
+            if (i + AHEAD < N)
+                f[i % AHEAD] = from[(i + AHEAD) * 64];
+            __builtin_amdgcn_sched_barrier(0x6);  // (VALU and SALU instructions may move across)
+        }
+    }
+};
+
+// A shared workgroup: rows [row0, row0 + 128 RT) of KV head h over range `split` of the prefix, wave w
+// the 16 RT from row0 + 16 RT w. A stage is NR records: K operands [chunk][a][j][lane] in a ring of
+// three and V operands [chunk][n][lane] in a ring of two (16 KB each at most). Wave w converts chunk
+// w % 4 (64 channels of a record) of K and of V, the tokens of half w / 4.
+//
+// One barrier a stage: while stage t is used, K of t + 2 and V of t + 1 are written. K(t + 2) takes the
+// place of K(t - 1) and V(t + 1) that of V(t - 1), last read before the barrier that ended t - 1; the
+// reads of K(t + 1) begin before the barrier that ends t.
+// (Holding waves 4-7 half a stage behind waves 0-3, so that one wave of a SIMD has the matrix unit while
+// the other converts and weighs, took four barriers a stage and came out even.)
+template <int FMT, int D, int NT, int RT>
+__device__ __forceinline__ void attend_shared(const AttendArgs &A, int split, int h, int row0, uint4 *lds)
+{
+    constexpr int NP = Rec<FMT, D>::NP, NR = stage_records(D);
+    constexpr int STAGE = 1024;  // uint4 of a stage's K or V
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i16 = lane & 15, g = lane >> 4;
+    const int nrows = A.B * A.Q * A.G, tokens = A.prefix_len;
+    const Range range = split_range(tokens, A.prefix_splits, split);
+    if (range.begin >= range.end)
+        return;
+    const int wrow = row0 + wave * 16 * RT;
+    const bool active = wrow < nrows;
+    const int limit = min(tokens, range.end * kTile);
+
+    const Records<FMT, D> recs(A, A.prefix_table, h);
+    // this wave's half chunk of each stage: chunk cp of the stage's record cr, half a
+    const int unit = wave & 3, cr = unit / NP, cp = unit & (NP - 1), a = wave >> 2;
+    const bool converts = cr < NR;
+    uint4 *const kring = lds, *const vring = lds + 3 * STAGE;
+    Half<FMT> kraw, vraw;
+    uint32_t ke, ve;
+    const uint8_t *krec = nullptr, *vrec = nullptr;  // the records to load next, K a stage ahead of V
+    // (records past the range: their place is the last one's, they are loaded and not used)
+    auto clamped = [&](int t0) { return min(t0 + cr, range.end - 1); };
+    auto load_stage = [&] {
+        if (!converts)
+            return;
+        load_half<FMT>(krec, cp, a, lane, kraw);
+        load_half<FMT>(vrec + Rec<FMT, D>::V, cp, a, lane, vraw);
+        ke = *reinterpret_cast<const uint8_t *>(krec + Rec<FMT, D>::KE + cp * 2 + a + k_exps<FMT, D>(lane));
+        ve = *reinterpret_cast<const uint32_t *>(vrec + Rec<FMT, D>::VE + cp * 8 + a * 4 + v_exps<FMT, D>(lane));
+    };
+    auto put_k = [&](uint4 *stage) {
+        if (!converts)
+            return;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            stage[(unit * 4 + a * 2 + j) * 64 + lane] =
+                __builtin_bit_cast(uint4, k_frag<FMT>(kraw, j, scale_of(ke, 0)));
+    };
+    auto put_v = [&](int t0, uint4 *stage) {
+        if (!converts)
+            return;
+        if ((t0 + cr + 1) * kTile > limit) {  // past the end: V must not meet a weight of zero as NaN
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                if ((t0 + cr) * kTile + 16 * a + 4 * g + r >= limit)
+                    v_clear<FMT>(vraw, ve, r);
+        }
+        uint2 f[4];
+        v_half<FMT>(vraw, ve, f);
+#pragma unroll
+        for (int n = 0; n < 4; n++)
+            reinterpret_cast<uint2 *>(stage + (unit * 4 + n) * 64 + lane)[a] = f[n];
+    };
+    const int t_first = range.begin;
+    const auto record = [&](int t0) { return recs.at(recs.page(clamped(t0)), clamped(t0)); };
+    // the first two stages' loads go out before q's: K and V of the first, K of the second
+    krec = vrec = record(t_first);
+    load_stage();
+    const Half<FMT> k0 = kraw, v0 = vraw;
+    const uint32_t ke0 = ke, ve0 = ve;
+    krec = vrec = record(t_first + NR);
+    load_stage();
+
+    bf16x8_t q[RT][NP * 2][NT];
+    State<NP> st[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int row = wrow + 16 * rt + i16;
+        const Row r = row_of<false>(A, 0, h, row < nrows ? row : 0);
+        load_q<NT, NP * 2>(A, r.q + 16 * g, row < nrows, q[rt]);
+        st[rt].clear();
+    }
+    const Half<FMT> k1 = kraw, v1 = vraw;
+    const uint32_t ke1 = ke, ve1 = ve;
+    kraw = k0;
+    vraw = v0;
+    ke = ke0;
+    ve = ve0;
+    put_k(kring);
+    put_v(t_first, vring);
+    kraw = k1;
+    ke = ke1;
+    put_k(kring + STAGE);
+    krec = record(t_first + 2 * NR);
+    load_stage();  // K of the third stage; V of the second is in hand
+    vraw = v1;
+    ve = ve1;
+    const uint8_t *vnext = krec;
+    int page = recs.page(clamped(t_first + 3 * NR));
+    // (two where a third would spill: 8-bit codes, 32 rows of 256 channels, 172 us -> 162 with 32,769 tokens)
+    ReadAhead<FMT == PN_CACHE_MXFP8 && D == 256 && RT == 2 ? 2 : 3> ahead;
+    __syncthreads();
+
+    int kslot = 0, vslot = 0;  // rings' places of stage t0
+    if (active)
+        ahead.begin(kring + lane);
+    for (int t0 = t_first; t0 < range.end; t0 += NR) {
+        const uint4 *const kstage = kring + kslot * STAGE + lane;
+        const uint4 *const vstage = vring + vslot * STAGE + lane;
+        kslot = kslot == 2 ? 0 : kslot + 1;
+        vslot ^= 1;
+        vrec = vnext;
+        krec = vnext = recs.at(page, clamped(t0 + 3 * NR));
+        f32x4_t s[RT][NR][2];
+        bf16x8_t w[RT][NR][NT];
+        if (active) {
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                for (int c = 0; c < NR; c++)
+                    s[rt][c][0] = s[rt][c][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            ahead.template run<NR * NP * 4>(kstage, [&](int i, bf16x8_t kf) {
+                const int c = i / (NP * 4), p = (i >> 2) % NP, b = (i >> 1) & 1, j = i & 1;
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+                        s[rt][c][b] = mfma(kf, q[rt][p * 2 + j][n], s[rt][c][b]);
+            });
+        }
+        page = recs.page(clamped(t0 + 4 * NR));  // here, where no LDS read is waited for with it
+        if (active) {
+            if ((t0 + NR) * kTile > limit) {
+#pragma unroll
+                for (int c = 0; c < NR; c++)
+#pragma unroll
+                    for (int b = 0; b < 2; b++)
+#pragma unroll
+                        for (int r = 0; r < 4; r++)
+                            if ((t0 + c) * kTile + 16 * b + 4 * g + r >= limit) {
+#pragma unroll
+                                for (int rt = 0; rt < RT; rt++)
+                                    s[rt][c][b][r] = -INFINITY;
+                            }
+            }
+            weigh<NT, NP, NR, RT>(s, A.scale, st, w);
+            __builtin_amdgcn_sched_barrier(0);  // (the scores' registers are free by now)
+            ahead.begin(vstage);
+            ahead.template run<NR * NP * 4>(vstage, [&](int i, bf16x8_t vf) {
+                const int c = i / (NP * 4), p = (i >> 2) % NP, n = i & 3;
 #pragma unroll
                 for (int rt = 0; rt < RT; rt++)
 #pragma unroll
                     for (int e = 0; e < NT; e++)
-                        O[rt][p][n] = mfma(vf[n],
-                                           __builtin_bit_cast(bf16x8_t, make_uint4(pw[rt][e][0], pw[rt][e][1],
-                                                                                   pw[rt][e][2], pw[rt][e][3])),
-                                           O[rt][p][n]);
+                        st[rt].O[p][n] = mfma(vf, w[rt][c][e], st[rt].O[p][n]);
+            });
+            ahead.begin(kring + kslot * STAGE + lane);
         }
-        if (more)
-            load_v<FMT, D>(next, lane, vr);
+        put_k(kring + (kslot == 2 ? 0 : kslot + 1) * STAGE);
+        put_v(t0 + NR, vring + vslot * STAGE);
+        load_stage();
+        __syncthreads();
     }
 
-    // join the four waves, a tile of 16 rows at a time: lds holds their O, then m and l
-    constexpr int PAD = D + 4;
-    float *const mls = lds + 4 * 16 * PAD;  // [wave][row][2]
+    const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
-        const float lsum = over_groups_sum(l[rt]);
-        if (rt > 0)
-            __syncthreads();
-#pragma unroll
-        for (int p = 0; p < NP; p++)
-#pragma unroll
-            for (int r = 0; r < 4; r++)
-                *reinterpret_cast<f32x4_t *>(lds + (wave * 16 + i16) * PAD + 64 * p + 16 * g + 4 * r) =
-                    f32x4_t{O[rt][p][0][r], O[rt][p][1][r], O[rt][p][2][r], O[rt][p][3][r]};
-        if (g == 0) {
-            mls[(wave * 16 + i16) * 2] = m[rt];
-            mls[(wave * 16 + i16) * 2 + 1] = lsum;
-        }
-        __syncthreads();
-        // thread = row * 16 + channel group
-        const int jr = threadIdx.x >> 4, cg = threadIdx.x & 15;
-        const int row = row0 + 16 * rt + jr;
+        const int row = wrow + 16 * rt + i16;
+        const float lsum = over_groups_sum(st[rt].l);
         if (row < nrows) {
-            float top = -INFINITY, sum = 0.0f, f[4];
-            bool saw[4];
+            const Row r = row_of<false>(A, 0, h, row);
+            float *const to = A.part + (split * rows + r.out) * D + 16 * g;
 #pragma unroll
-            for (int w = 0; w < 4; w++)
-                top = fmaxf(top, mls[(w * 16 + jr) * 2]);
+            for (int p = 0; p < NP; p++)
 #pragma unroll
-            for (int w = 0; w < 4; w++) {
-                // l = 0 only where a wave saw no token (l is NaN where its scores are)
-                const float lw = mls[(w * 16 + jr) * 2 + 1];
-                saw[w] = lw != 0.0f;
-                f[w] = saw[w] ? __builtin_amdgcn_exp2f(mls[(w * 16 + jr) * 2] - top) : 0.0f;
-                sum += f[w] * lw;
-            }
-            const int qt = row / A.G;
-            const int b = OWN ? b0 : qt / A.Q, i = OWN ? qt : qt - b * A.Q;
-            const int64_t orow = ((int64_t)b * A.Q + i) * A.Hq + h * A.G + (row - qt * A.G);
-            const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
-            const int64_t slot = (OWN ? A.prefix_splits : 0) + split;
-            if (A.direct && i >= nq)
-                sum = 0.0f;  // not a query token of this sequence
-            const bool none = sum == 0.0f;
-            const float inv = 1.0f / sum;
-#pragma unroll
-            for (int p = 0; p < NP; p++) {
-                f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < 4; w++)
-                    if (saw[w])
-                        v += f[w] * *reinterpret_cast<const f32x4_t *>(lds + (w * 16 + jr) * PAD + 64 * p + 4 * cg);
-                const int64_t at = orow * D + 64 * p + 4 * cg;
-                if (A.direct) {
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        store_elem(A.type, A.out, at + e, none ? 0.0f : v[e] * inv);
-                } else {
-                    *reinterpret_cast<f32x4_t *>(A.part + slot * rows * D + at) = v;
-                }
-            }
-            if (cg == 0) {
-                if (!A.direct)
-                    A.part_ml[slot * rows + orow] = make_float2(top, sum);
-                else if (A.lse)
-                    A.lse[orow] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-            }
+                for (int e = 0; e < 4; e++)
+                    *reinterpret_cast<f32x4_t *>(to + 64 * p + 4 * e) = f32x4_t{
+                        st[rt].O[p][0][e], st[rt].O[p][1][e], st[rt].O[p][2][e], st[rt].O[p][3][e]};
+            if (g == 0)
+                A.part_ml[split * rows + r.out] = make_float2(-st[rt].base, lsum);
         }
     }
 }
 
-// Workgroups: first the prefix's [row block][KV head and range], then [range][sequence][row block][KV
-// head] of the own tokens. RP, RO: tiles of 16 rows a wave holds in the prefix (0: no prefix) and in
-// the own tokens.
-template <int FMT, int D, int NT, int RP, int RO>
-__global__ void __launch_bounds__(256) attend_kernel(AttendArgs A)
+// Workgroups: first the prefix's [row block][range][KV head], so that the row blocks that read the
+// same tokens run on one XCD where their number allows, then the own tokens' [range][sequence][row
+// block][KV head]. RT: tiles of 16 rows a wave holds in the prefix's shared workgroups (0: they are
+// stream workgroups, if any).
+template <int FMT, int D, int NT, int RT>
+__global__ void __launch_bounds__(512, 2) attend_kernel(AttendArgs A)
 {
-    extern __shared__ float lds[];
+    extern __shared__ uint4 lds[];
     int id = blockIdx.x;
-    if constexpr (RP > 0) {
-        const int each = A.c.heads * A.prefix_splits;
-        if (id < each * A.prefix_blocks) {
-            const int block = id / each, rest = id - block * each;
-            const int split = rest / A.c.heads, h = rest - split * A.c.heads;
-            attend_part<FMT, D, NT, RP, false>(A, split, 0, h, block * 16 * RP, lds);
-            return;
-        }
-        id -= each * A.prefix_blocks;
+    const int each = A.c.heads * A.prefix_splits;
+    if (id < each * A.prefix_blocks) {
+        const int block = id / each, rest = id - block * each;
+        const int split = rest / A.c.heads, h = rest - split * A.c.heads;
+        if constexpr (RT > 0)
+            attend_shared<FMT, D, NT, RT>(A, split, h, block * 128 * RT, lds);
+        else
+            attend_stream<FMT, D, NT, false>(A, split, 0, h, block * 16 * A.prefix_tiles, A.prefix_tiles, lds);
+        return;
     }
+    id -= each * A.prefix_blocks;
     const int h = id % A.c.heads;
     id /= A.c.heads;
     const int block = id % A.own_blocks;
     id /= A.own_blocks;
     const int b = id % A.B;
-    attend_part<FMT, D, NT, RO, true>(A, id / A.B, b, h, block * 16 * RO, lds);
+    attend_stream<FMT, D, NT, true>(A, id / A.B, b, h, block * 16 * A.own_tiles, A.own_tiles, lds);
 }
 
-// Joins the ranges of one row: a wave a row, lane = channels D / 64 * lane ...
+// The ranges that a row has results of: `n`, the first `np` of the prefix.
+struct Live {
+    int np, n, prefix_splits;
+    __device__ __forceinline__ Live(const AttendArgs &A, int64_t row) : prefix_splits(A.prefix_splits)
+    {
+        const int qt = A.by_Hq.of((int)row), b = A.by_Q.of(qt), i = qt - b * A.Q;
+        np = A.prefix_splits ? live_ranges(A.prefix_len, A.prefix_splits) : 0;
+        n = np + live_ranges(own_tokens(A, b), A.own_splits);
+        if (i >= query_tokens(A, b))
+            n = np = 0;
+    }
+    __device__ __forceinline__ int64_t slot(int k) const { return k < np ? k : prefix_splits + k - np; }
+};
+
+// Few rows: joins the ranges of 64 channels of a row in a workgroup, thread = four channels of every
+// 16th range.
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs A)
 {
-    constexpr int C = D / 64;
-    typedef float vec __attribute__((ext_vector_type(C)));
-    const int lane = threadIdx.x & 63;
+    constexpr int NP = D / 64;
+    constexpr int AHEAD = 4;  // ranges a thread has in flight
+    __shared__ f32x4_t part[16][16];
+    __shared__ float sums[16];
+    const int lane = threadIdx.x & 63, cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
-    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row >= rows)
-        return;
-    const int qt = (int)(row / A.Hq), b = qt / A.Q, i = qt - b * A.Q;
-    int np = live_ranges(A.prefix_len, A.prefix_splits ? A.prefix_splits : 1);
-    int n = np + live_ranges(own_tokens(A, b), A.own_splits);
-    if (i >= query_tokens(A, b))
-        n = np = 0;
-    const auto slot = [&](int k) -> int64_t { return k < np ? k : A.prefix_splits + k - np; };
-    float top = -INFINITY;
+    const int64_t row = blockIdx.x / NP;
+    const int p = blockIdx.x - (int)row * NP;
+    const Live live(A, row);
+    const int n = live.n;
+    const auto slot = [&](int k) { return live.slot(k); };
+    f32x4_t o[AHEAD];
+    float2 ml[AHEAD];
+    const auto load = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; k++) {
+            const int r = k0 + 16 * k;
+            ml[k] = r < n ? A.part_ml[slot(r) * rows + row] : make_float2(0.0f, 0.0f);
+            o[k] = r < n ? *reinterpret_cast<const f32x4_t *>(A.part + (slot(r) * rows + row) * D + 64 * p + 4 * cg)
+                         : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+    load(rg);
+    float top = -INFINITY;  // every wave finds the maximum by itself
     for (int k = lane; k < n; k += 64)
         top = fmaxf(top, A.part_ml[slot(k) * rows + row].x);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor(top, o, 64));
+    for (int s = 32; s > 0; s >>= 1)
+        top = fmaxf(top, __shfl_xor(top, s, 64));
     float sum = 0.0f;
-    vec acc = {};
-    for (int k0 = 0; k0 < n; k0 += 64) {
-        float f = 0.0f;
-        if (k0 + lane < n) {
-            const float2 ml = A.part_ml[slot(k0 + lane) * rows + row];
-            f = ml.y != 0.0f ? __builtin_amdgcn_exp2f(ml.x - top) : 0.0f;
-            sum += f * ml.y;
-        }
-        const int most = min(64, n - k0);
-#pragma unroll 8
-        for (int k = 0; k < most; k++) {
-            const float fk = __builtin_bit_cast(
-                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), k));
-            const vec o = *reinterpret_cast<const vec *>(A.part + (slot(k0 + k) * rows + row) * D + C * lane);
-            acc += fk * o;
-        }
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = rg; k0 < n; k0 += 16 * AHEAD) {
+        if (k0 > rg)
+            load(k0);
+#pragma unroll
+        for (int k = 0; k < AHEAD; k++)
+            if (ml[k].y != 0.0f) {
+                const float f = __builtin_amdgcn_exp2f(ml[k].x - top);
+                sum += f * ml[k].y;
+                acc += f * o[k];
+            }
     }
-    sum = wave_sum(sum);
+    part[rg][cg] = acc;
+    if (cg == 0)
+        sums[rg] = sum;
+    __syncthreads();
+    if (rg != 0)
+        return;
+    sum = 0.0f;
+    acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+        sum += sums[r];
+        acc += part[r][cg];
+    }
     const bool none = sum == 0.0f;
     const float inv = 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < C; e++)
-        store_elem(A.type, A.out, row * D + C * lane + e, none ? 0.0f : acc[e] * inv);
-    if (lane == 0 && A.lse)
+    store4(A.type, A.out, row * D + 64 * p + 4 * cg, none ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : acc * inv);
+    if (p == 0 && cg == 0 && A.lse)
         A.lse[row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-template <int FMT, int D, int NT, int RP, int RO>
+// Many rows: a wave joins 256 / D rows, D / 4 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_rows_kernel(AttendArgs A)
+{
+    constexpr int L = D / 4;  // lanes a row
+    const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = at / L;
+    const int cg = (int)(at % L);
+    if (row >= rows)
+        return;
+    const Live live(A, row);
+    float m = -INFINITY, sum = 0.0f;
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < live.n; k0 += 8) {  // eight ranges in flight
+        float2 ml[8];
+        f32x4_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int64_t i = live.slot(min(k0 + k, live.n - 1)) * rows + row;
+            ml[k] = A.part_ml[i];
+            o[k] = *reinterpret_cast<const f32x4_t *>(A.part + i * D + 4 * cg);
+            if (k0 + k >= live.n)
+                ml[k] = make_float2(-INFINITY, 0.0f);
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            top = fmaxf(top, ml[k].x);
+        const float f0 = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        sum *= f0;
+        acc *= f0;
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (ml[k].y != 0.0f) {
+                const float f = __builtin_amdgcn_exp2f(ml[k].x - m);
+                sum += f * ml[k].y;
+                acc += f * o[k];
+            }
+    }
+    const bool none = sum == 0.0f;
+    const float inv = 1.0f / sum;
+    store4(A.type, A.out, row * D + 4 * cg, none ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : acc * inv);
+    if (cg == 0 && A.lse)
+        A.lse[row] = none ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <int FMT, int D, int NT, int RT>
 static int launch_attend(const AttendArgs &A, hipStream_t s)
 {
-    constexpr auto kern = attend_kernel<FMT, D, NT, RP, RO>;
-    constexpr int bytes = (4 * 16 * (D + 4) + 4 * 16 * 2) * 4;
-    if (!lds_limit_once<kern>(bytes))
+    constexpr auto kern = attend_kernel<FMT, D, NT, RT>;
+    // q operands of a stream workgroup, the joining of its waves, or a shared one's two stages
+    const int tiles = std::max(A.own_tiles, RT > 0 ? 1 : A.prefix_tiles);
+    const int bytes = std::max(std::max(tiles * (D / 32) * NT * 1024, kWaves * 16 * (D + 4 + 2) * 4), RT > 0 ? 5 * 16384 : 0);
+    if (!lds_limit_once<kern>(160 * 1024))
         return PN_ERR_HIP;
+    const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
     const int64_t grid = (int64_t)A.c.heads * A.prefix_splits * A.prefix_blocks +
                          (int64_t)A.own_splits * A.B * A.own_blocks * A.c.heads;
-    if (grid > INT32_MAX)
+    if (grid > INT32_MAX || rows > INT32_MAX / (D / 64))
         return PN_ERR_SHAPE;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), bytes, s, A);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kWaves * 64), bytes, s, A);
     const int st = launch_status();
     if (st != PN_OK || A.direct)
         return st;
-    const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
-    hipLaunchKernelGGL((attend_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, A);
+    // a wave a row where the rows fill the CUs with four waves each: 960 rows, 18 ranges
+    if (rows >= 1024)
+        hipLaunchKernelGGL((attend_join_rows_kernel<D>), dim3((unsigned)((rows * (D / 4) + 255) / 256)),
+                           dim3(256), 0, s, A);
+    else
+        hipLaunchKernelGGL((attend_join_kernel<D>), dim3((unsigned)(rows * (D / 64))), dim3(256), 0, s, A);
     return launch_status();
 }
 
-// rp, ro: the rows a wave holds, as attend_cut chose them
 template <int FMT, int D, int NT>
-static int launch_rows(const AttendArgs &A, int rp, int ro, hipStream_t s)
+static int launch_tiles(const AttendArgs &A, hipStream_t s)
 {
-    constexpr int MOST = D == 256 || NT == 2 ? 2 : 4;
-    if (ro == 1)
-        return rp == 0   ? launch_attend<FMT, D, NT, 0, 1>(A, s)
-               : rp == 1 ? launch_attend<FMT, D, NT, 1, 1>(A, s)
-                         : launch_attend<FMT, D, NT, MOST, 1>(A, s);
-    return rp == 0 ? launch_attend<FMT, D, NT, 0, 2>(A, s) : launch_attend<FMT, D, NT, MOST, 2>(A, s);
+    constexpr int MOST = shared_tiles(D, NT);
+    if (A.shared_tiles == 0)
+        return launch_attend<FMT, D, NT, 0>(A, s);
+    if (A.shared_tiles == 1)
+        return launch_attend<FMT, D, NT, 1>(A, s);
+    if (MOST >= 2 && A.shared_tiles == 2)
+        return launch_attend<FMT, D, NT, MOST >= 2 ? 2 : 1>(A, s);
+    return launch_attend<FMT, D, NT, MOST>(A, s);
 }
 
-// Launches format FMT, one source file each.
+// Launches format FMT, one source file each. parts: of q and the weights (1, 2, 3).
 template <int FMT>
-int launch_format(const AttendArgs &A, int dim, bool two, int rp, int ro, hipStream_t s);
+int launch_format(const AttendArgs &A, int dim, int parts, hipStream_t s);
 
+#define PN_ATTEND_DIM(FMT, D)                                                                      \
+    return parts == 1   ? launch_tiles<FMT, D, 1>(A, s)                                            \
+           : parts == 2 ? launch_tiles<FMT, D, 2>(A, s)                                            \
+                        : launch_tiles<FMT, D, 3>(A, s);
 #define PN_ATTEND_FORMAT(FMT)                                                                      \
     template <>                                                                                    \
-    int launch_format<FMT>(const AttendArgs &A, int dim, bool two, int rp, int ro, hipStream_t s)  \
+    int launch_format<FMT>(const AttendArgs &A, int dim, int parts, hipStream_t s)                 \
     {                                                                                              \
-        switch (dim) {                                                                             \
-        case 64: return two ? launch_rows<FMT, 64, 2>(A, rp, ro, s) : launch_rows<FMT, 64, 1>(A, rp, ro, s); \
-        case 128: return two ? launch_rows<FMT, 128, 2>(A, rp, ro, s) : launch_rows<FMT, 128, 1>(A, rp, ro, s); \
-        default: return two ? launch_rows<FMT, 256, 2>(A, rp, ro, s) : launch_rows<FMT, 256, 1>(A, rp, ro, s); \
+        if (dim == 64) {                                                                           \
+            PN_ATTEND_DIM(FMT, 64)                                                                 \
+        } else if (dim == 128) {                                                                   \
+            PN_ATTEND_DIM(FMT, 128)                                                                \
         }                                                                                          \
+        PN_ATTEND_DIM(FMT, 256)                                                                    \
     }
 
 }  // namespace pn

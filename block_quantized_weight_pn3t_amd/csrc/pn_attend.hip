@@ -5,13 +5,15 @@
 namespace pn {
 
 template <>
-int launch_format<PN_CACHE_MXFP8>(const AttendArgs &A, int dim, bool two, int rp, int ro, hipStream_t s);
+int launch_format<PN_CACHE_MXFP8>(const AttendArgs &A, int dim, int parts, hipStream_t s);
 template <>
-int launch_format<PN_CACHE_MXFP4>(const AttendArgs &A, int dim, bool two, int rp, int ro, hipStream_t s);
+int launch_format<PN_CACHE_MXFP4>(const AttendArgs &A, int dim, int parts, hipStream_t s);
 
-// How a call is cut: rows a wave holds, row blocks and token ranges.
+static int parts_of(int type) { return type == PN_BF16 ? 1 : type == PN_F16 ? 2 : 3; }
+
+// How a call is cut: rows a wave or workgroup holds, row blocks and token ranges (as in AttendArgs).
 struct Cut {
-    int rp, ro;  // tiles of 16 rows (prefix, own)
+    int shared_tiles, prefix_tiles, own_tiles;
     int prefix_splits, prefix_blocks, own_splits, own_blocks;
     bool direct;
     int64_t rows;
@@ -40,22 +42,36 @@ static int attend_check(const pn_cache *cache, const pn_attend_args *a, CacheVie
 static Cut attend_cut(const pn_cache *cache, const pn_attend_args *a)
 {
     const int G = a->Hq / cache->heads;
-    const bool two = a->type != PN_BF16;
-    Cut t;
+    Cut t = {};
     const int64_t own_rows = (int64_t)a->Q * G, prefix_rows = own_rows * a->B;
     const int64_t own_records = (int64_t)a->table_width * (cache->page / kTile);
     const int64_t prefix_records = (a->prefix_len + kTile - 1) / kTile;
-    t.ro = own_rows <= 16 ? 1 : 2;
-    t.rp = prefix_records == 0 ? 0 : prefix_rows <= 16 ? 1 : cache->dim == 256 || two ? 2 : 4;
-    t.own_blocks = (int)((own_rows + 16 * t.ro - 1) / (16 * t.ro));
-    t.prefix_blocks = t.rp ? (int)((prefix_rows + 16 * t.rp - 1) / (16 * t.rp)) : 0;
-    // two workgroups a CU, at least one record a wave
-    const int64_t want = 2 * device_cus();
-    auto splits = [&](int64_t items, int64_t records) {
-        return (int)std::max<int64_t>(1, std::min((want + items - 1) / items, (records + 3) / 4));
-    };
-    t.own_splits = splits((int64_t)a->B * cache->heads * t.own_blocks, own_records);
-    t.prefix_splits = t.rp ? splits((int64_t)cache->heads * t.prefix_blocks, prefix_records) : 0;
+    const int64_t cus = device_cus();  // a workgroup a CU fills it: 8 waves of up to 256 registers
+    const auto stream_tiles = [](int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; };
+    const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    t.own_tiles = stream_tiles(own_rows);
+    t.own_blocks = (int)up(own_rows, 16 * t.own_tiles);
+    // At least one record a wave. One range in all is written out at once; the second kernel that joins
+    // several takes 4 to 5 us with its launch, what a wave needs for about 512 / (dim * parts) records:
+    // 16 sequences of up to 777 tokens, 128 channels, bf16 9.3 us in one range, 8.5 + 4.7 in two; one of
+    // 1000 tokens, 256 channels, fp32 16.5 us in one, 9.6 + 3.7 in four.
+    const int64_t a_wave = up(own_records * t.own_tiles, kWaves);
+    const bool one = prefix_records == 0 && a_wave * cache->dim * parts_of(a->type) <= 512;
+    t.own_splits = one ? 1
+                       : (int)std::max<int64_t>(1, std::min(up(cus, (int64_t)a->B * cache->heads * t.own_blocks),
+                                                            a_wave));
+    if (prefix_records > 0 && prefix_rows <= 64) {
+        t.prefix_tiles = stream_tiles(prefix_rows);
+        t.prefix_blocks = 1;
+        t.prefix_splits = (int)std::min(up(cus, cache->heads), up(prefix_records * t.prefix_tiles, kWaves));
+    } else if (prefix_records > 0) {
+        const int most = shared_tiles(cache->dim, parts_of(a->type));
+        t.shared_tiles = prefix_rows <= 128 ? 1 : prefix_rows <= 256 ? std::min(2, most) : most;
+        t.prefix_blocks = (int)up(prefix_rows, 128 * t.shared_tiles);
+        // one round of workgroups, at least eight records each
+        t.prefix_splits = (int)std::max<int64_t>(1, std::min(cus / ((int64_t)cache->heads * t.prefix_blocks),
+                                                             up(prefix_records, 8)));
+    }
     t.direct = t.own_splits + t.prefix_splits == 1;
     t.rows = (int64_t)a->B * a->Q * a->Hq;
     t.workspace = t.direct ? 0 : (t.own_splits + t.prefix_splits) * t.rows * (cache->dim + 2) * 4;
@@ -111,14 +127,16 @@ extern "C" int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *w
     A.Q = a->Q;
     A.Hq = a->Hq;
     A.G = a->Hq / cache->heads;
+    A.by_G = FastDiv(A.G);
+    A.by_Q = FastDiv(A.Q);
+    A.by_Hq = FastDiv(A.Hq);
     A.q = a->q;
     A.q_seq = a->q_seq_stride;
     A.q_tok = a->q_token_stride;
     A.q_head = a->q_head_stride;
-    const int eight = size * 8 > 16 ? 4 : 8;  // elements of 16 bytes
-    A.q_vec = aligned(a->q, 16) && ((A.q_seq | A.q_tok | A.q_head) & (eight - 1)) == 0;
+    A.q_vec = aligned(a->q, 4 * size) && ((A.q_seq | A.q_tok | A.q_head) & 3) == 0;
     A.scale = fmaxf(fabsf(a->scale) * kLog2e, 0x1p-126f);
-    A.neg = a->scale < 0.0f;
+    A.sign = a->scale < 0.0f ? -1.0f : 1.0f;
     A.table = a->table;
     A.table_stride = a->table_stride;
     A.table_width = a->table_width;
@@ -126,6 +144,9 @@ extern "C" int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *w
     A.q_lens = a->q_lens;
     A.prefix_table = a->prefix_table;
     A.prefix_len = (int)a->prefix_len;
+    A.shared_tiles = t.shared_tiles;
+    A.prefix_tiles = t.prefix_tiles;
+    A.own_tiles = t.own_tiles;
     A.prefix_splits = t.prefix_splits;
     A.prefix_blocks = t.prefix_blocks;
     A.own_splits = t.own_splits;
@@ -136,8 +157,7 @@ extern "C" int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *w
     A.out = a->out;
     A.lse = a->lse;
     hipStream_t s = (hipStream_t)stream;
-    const bool two = a->type != PN_BF16;
     return cache->format == PN_CACHE_MXFP8
-               ? launch_format<PN_CACHE_MXFP8>(A, cache->dim, two, t.rp, t.ro, s)
-               : launch_format<PN_CACHE_MXFP4>(A, cache->dim, two, t.rp, t.ro, s);
+               ? launch_format<PN_CACHE_MXFP8>(A, cache->dim, parts_of(a->type), s)
+               : launch_format<PN_CACHE_MXFP4>(A, cache->dim, parts_of(a->type), s);
 }
