@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 __all__ = ["PN3T", "PN4T", "PNError", "row_bytes", "validate_rows", "validate_row",
            "dequantize_rows", "dequantize_row", "gemv", "gemv_group", "quantize_rows", "hadamard_rows",
@@ -117,12 +118,12 @@ def _check(status: int, what: str):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        import torch
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
-        return C.c_void_p(stream)
-    return C.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _ptr(t) -> int:
@@ -328,31 +329,50 @@ def gemv_fp8row_ptr(codes_ptr, scales_ptr, N, K, x_ptr, M, y_ptr, stream_handle)
 
 
 # ---- microscaled cache, attention over it, verification of drafts ---------------------------------
+#
+# A decode step makes these calls one after another while each kernel runs for a few microseconds, so
+# a call's checks are single expressions that hold for good arguments; what is wrong with bad ones is
+# worked out afterwards.
 
-_TYPE_OF = {}
+class _Torch:
+    """torch's names that the checks below use, looked up once."""
+    f32 = None
 
-
-def _elem(t, name):
-    """The element type id of a plain tensor on the device."""
-    if not _TYPE_OF:
+    @classmethod
+    def load(cls):
         import torch
-        _TYPE_OF.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype not in _TYPE_OF:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return _TYPE_OF[t.dtype]
+        cls.i32, cls.i64, cls.u8 = torch.int32, torch.int64, torch.uint8
+        cls.kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        cls.stream = torch.cuda.current_stream
+        cls.f32 = torch.float32
+        return cls
 
 
-def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _names():
+    return _Torch if _Torch.f32 is not None else _Torch.load()
 
 
-def _ints(t, name, dtype, shape):
-    import torch
-    _dev(t, name, getattr(torch, dtype))
-    _shape(t, name, shape)
+def _is(t, dtype, shape):
+    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _refuse(t, name, dtype, shape):
+    """Says what is wrong with a tensor that _is() not what it has to be."""
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _elem(t, name, T):
+    """The element type id of a plain tensor on the device."""
+    kind = T.kinds.get(t.dtype)
+    if kind is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor of float32, bfloat16 or float16, got {t.dtype} "
+                         f"on {t.device}")
+    return kind
+
+
+def _handle(stream, T):
+    return T.stream().cuda_stream if stream is None else _stream(stream)
 
 
 def cache_page_bytes(format, heads, dim, page):
@@ -383,40 +403,49 @@ class Cache:
 def cache_write(cache, k, v, slots, stream=None):
     """Quantises k and v [T, heads, dim] (channels contiguous) into the cache; token t goes to
     slots[t] (int64), nowhere where that is outside the cache (pn_cache_write)."""
-    kind = _elem(k, "k")
-    shape = (k.shape[0], cache.heads, cache.dim)
-    _shape(k, "k", shape)
-    _shape(v, "v", shape)
-    if _elem(v, "v") != kind:
-        raise ValueError("k and v must have the same type")
-    if k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("the channels of k and v must be contiguous")
-    _ints(slots, "slots", "int64", shape[:1])
-    _check(_lib.pn_cache_write(cache.ref, kind, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                               v.stride(0), v.stride(1), slots.data_ptr(), shape[0], _stream(stream)),
-           "pn_cache_write")
+    T = _names()
+    kind = _elem(k, "k", T)
+    n = k.shape[0]
+    shape = (n, cache.heads, cache.dim)
+    kt, kh, kc = k.stride() if k.shape == shape else (0, 0, 0)
+    vt, vh, vc = v.stride() if v.shape == shape else (0, 0, 0)
+    if kc != 1 or vc != 1:
+        raise ValueError(f"k and v must have shape {shape} with contiguous channels, got "
+                         f"{tuple(k.shape)} and {tuple(v.shape)} with strides {k.stride()}, {v.stride()}")
+    if v.dtype is not k.dtype or not v.is_cuda:
+        raise ValueError("k and v must have the same type and be on the device")
+    if not _is(slots, T.i64, (n,)):
+        _refuse(slots, "slots", T.i64, (n,))
+    _check(_lib.pn_cache_write(cache.ref, kind, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                               slots.data_ptr(), n, _handle(stream, T)), "pn_cache_write")
 
 
 def cache_read(cache, slots, k, v, stream=None):
     """k and v [T, heads, dim] <- the cache's tokens at slots (int64); zeros for a slot outside it
     (pn_cache_read)."""
-    kind = _elem(k, "k")
-    shape = (slots.shape[0], cache.heads, cache.dim)
-    _ints(slots, "slots", "int64", shape[:1])
-    _dev(k, "k")
-    _dev(v, "v", k.dtype)
-    _shape(k, "k", shape)
-    _shape(v, "v", shape)
-    _check(_lib.pn_cache_read(cache.ref, kind, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                              _stream(stream)), "pn_cache_read")
+    T = _names()
+    kind = _elem(k, "k", T)
+    n = k.shape[0]
+    shape = (n, cache.heads, cache.dim)
+    if not _is(k, k.dtype, shape):
+        _refuse(k, "k", k.dtype, shape)
+    if not _is(v, k.dtype, shape):
+        _refuse(v, "v", k.dtype, shape)
+    if not _is(slots, T.i64, (n,)):
+        _refuse(slots, "slots", T.i64, (n,))
+    _check(_lib.pn_cache_read(cache.ref, kind, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                              _handle(stream, T)), "pn_cache_read")
 
 
 def attend_workspace_bytes(cache, q, table, prefix_len=0):
     """Device bytes that attend needs for q [B, Q, Hq, dim] and these tables."""
     B, Q, Hq, _ = q.shape
-    a = AttendArgs(type=_elem(q, "q"), B=B, Q=Q, Hq=Hq, scale=1.0, table_width=table.shape[1],
+    a = AttendArgs(type=_elem(q, "q", _names()), B=B, Q=Q, Hq=Hq, scale=1.0, table_width=table.shape[1],
                    prefix_len=prefix_len)
     return int(_lib.pn_attend_workspace_bytes(cache.ref, C.addressof(a)))
+
+
+_pack_attend = struct.Struct("@iiiiPqqqfPqiPPPqPP").pack  # pn_attend_args, a third of AttendArgs()'s time
 
 
 def attend(cache, q, table, lens, out, lse=None, workspace=None, prefix_table=None, prefix_len=0,
@@ -427,45 +456,61 @@ def attend(cache, q, table, lens, out, lse=None, workspace=None, prefix_table=No
     last of the own tokens are the queries', each sees up to itself. lse fp32[B, Q, Hq] <- the log of
     the sum of exp(scores). q_lens int32[B]: query tokens that a sequence has, Q unless given. scale:
     dim ** -0.5 unless given. workspace: a uint8 tensor of attend_workspace_bytes."""
-    kind = _elem(q, "q")
+    T = _names()
+    kind = _elem(q, "q", T)
     if q.dim() != 4 or q.shape[3] != cache.dim:
         raise ValueError(f"q must be [B, Q, Hq, {cache.dim}], got {tuple(q.shape)}")
-    B, Q, Hq, _ = q.shape
-    qs = q.stride()
-    if qs[3] != 1:
+    B, Q, Hq, dim = shape = q.shape
+    qb, qt, qh, qc = q.stride()
+    if qc != 1:
         raise ValueError("the channels of q must be contiguous")
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be [{B}, width] with contiguous rows, got {tuple(table.shape)}")
-    import torch
-    if table.dtype != torch.int32 or not table.is_cuda:
-        raise ValueError("table must be an int32 device tensor")
-    _ints(lens, "lens", "int32", (B,))
-    _dev(out, "out", q.dtype)
-    _shape(out, "out", q.shape)
+    if table.dim() != 2 or table.shape[0] != B or table.dtype is not T.i32 or not table.is_cuda:
+        raise ValueError(f"table must be an int32 device tensor [{B}, width], got {table.dtype} "
+                         f"{tuple(table.shape)} on {table.device}")
+    width = table.shape[1]
+    row, column = table.stride()
+    if column != 1 and width > 1:
+        raise ValueError("the rows of table must be contiguous")
+    if not _is(lens, T.i32, (B,)):
+        _refuse(lens, "lens", T.i32, (B,))
+    if not _is(out, q.dtype, shape):
+        _refuse(out, "out", q.dtype, shape)
+    lse_at = q_lens_at = prefix_at = work_at = work_bytes = 0
     if lse is not None:
-        _dev(lse, "lse", torch.float32)
-        _shape(lse, "lse", (B, Q, Hq))
+        if not _is(lse, T.f32, (B, Q, Hq)):
+            _refuse(lse, "lse", T.f32, (B, Q, Hq))
+        lse_at = lse.data_ptr()
     if q_lens is not None:
-        _ints(q_lens, "q_lens", "int32", (B,))
+        if not _is(q_lens, T.i32, (B,)):
+            _refuse(q_lens, "q_lens", T.i32, (B,))
+        q_lens_at = q_lens.data_ptr()
     if prefix_len < 0:
         raise ValueError("prefix_len must not be negative")
     if prefix_len:
-        _dev(prefix_table, "prefix_table", torch.int32)
+        _dev(prefix_table, "prefix_table", T.i32)
         if prefix_table.numel() * cache.page < prefix_len:
             raise ValueError("prefix_table has too few pages for prefix_len")
+        prefix_at = prefix_table.data_ptr()
     if workspace is not None:
-        _dev(workspace, "workspace", torch.uint8)
-    a = AttendArgs(kind, B, Q, Hq, q.data_ptr(), qs[0], qs[1], qs[2],
-                   cache.dim ** -0.5 if scale is None else scale, table.data_ptr(), table.stride(0),
-                   table.shape[1], lens.data_ptr(), _ptr(q_lens), _ptr(prefix_table), prefix_len,
-                   out.data_ptr(), _ptr(lse))
-    _check(_lib.pn_attend(cache.ref, C.addressof(a), _ptr(workspace),
-                          0 if workspace is None else workspace.numel(), _stream(stream)), "pn_attend")
+        _dev(workspace, "workspace", T.u8)
+        work_at, work_bytes = workspace.data_ptr(), workspace.numel()
+    a = _pack_attend(kind, B, Q, Hq, q.data_ptr(), qb, qt, qh, dim ** -0.5 if scale is None else scale,
+                     table.data_ptr(), row, width, lens.data_ptr(), q_lens_at, prefix_at, prefix_len,
+                     out.data_ptr(), lse_at)
+    _check(_lib.pn_attend(cache.ref, a, work_at, work_bytes, _handle(stream, T)), "pn_attend")
 
 
 def verify_workspace_bytes(B, V):
     """Device bytes that verify needs for B sequences over V tokens."""
     return int(_lib.pn_verify_workspace_bytes(B, V))
+
+
+def _row_spacing(t, name, n):
+    """The spacing of the n rows a sequence that t [B, n, V] has."""
+    b, row, v = t.stride()
+    if (v != 1 and t.shape[2] > 1) or (t.shape[0] > 1 and n > 1 and b != n * row):
+        raise ValueError(f"the rows of {name} must be contiguous and evenly spaced")
+    return row if n > 1 else b
 
 
 def verify(p, q, draft, u_accept, u_sample, tokens, accepted, workspace, n_draft=None, stream=None):
@@ -475,36 +520,37 @@ def verify(p, q, draft, u_accept, u_sample, tokens, accepted, workspace, n_draft
     int32[B, K + 1] <- the accepted drafts, the token after them, then -1; accepted int32[B] <- their
     number. n_draft int32[B]: drafts that a sequence has, K unless given. workspace: a uint8 tensor
     of verify_workspace_bytes."""
-    import torch
-    kind = _elem(p, "p")
-    B, K = draft.shape
+    T = _names()
+    kind = _elem(p, "p", T)
+    if draft.dim() != 2:
+        raise ValueError(f"draft must be [B, K], got {tuple(draft.shape)}")
+    B, K = shape = draft.shape
     if p.dim() != 3 or p.shape[0] != B or p.shape[1] != K + 1:
         raise ValueError(f"p must be [{B}, {K + 1}, V], got {tuple(p.shape)}")
     V = p.shape[2]
-
-    def rows(t, name, n):
-        if t.stride(2) != 1 or (B > 1 and t.stride(0) != n * t.stride(1)):
-            raise ValueError(f"the rows of {name} must be contiguous and evenly spaced")
-        return t.stride(1) if n > 1 else t.stride(0)
-    ps = rows(p, "p", K + 1)
-    qs = 0
+    p_row, q_row, q_at, n_at = _row_spacing(p, "p", K + 1), 0, 0, 0
     if q is not None:
-        if _elem(q, "q") != kind:
-            raise ValueError("p and q must have the same type")
-        _shape(q, "q", (B, K, V))
+        if q.dtype is not p.dtype or q.shape != (B, K, V) or not q.is_cuda:
+            raise ValueError(f"q must be a device tensor of {p.dtype} [{B}, {K}, {V}], got {q.dtype} "
+                             f"{tuple(q.shape)} on {q.device}")
         if K:
-            qs = rows(q, "q", K)
-    _ints(draft, "draft", "int32", (B, K))
-    _dev(u_accept, "u_accept", torch.float32)
-    _shape(u_accept, "u_accept", (B, K))
-    _dev(u_sample, "u_sample", torch.float32)
-    _shape(u_sample, "u_sample", (B,))
-    _ints(tokens, "tokens", "int32", (B, K + 1))
-    _ints(accepted, "accepted", "int32", (B,))
+            q_row, q_at = _row_spacing(q, "q", K), q.data_ptr()
+    if not _is(draft, T.i32, shape):
+        _refuse(draft, "draft", T.i32, shape)
+    if not _is(u_accept, T.f32, shape):
+        _refuse(u_accept, "u_accept", T.f32, shape)
+    if not _is(u_sample, T.f32, (B,)):
+        _refuse(u_sample, "u_sample", T.f32, (B,))
+    if not _is(tokens, T.i32, (B, K + 1)):
+        _refuse(tokens, "tokens", T.i32, (B, K + 1))
+    if not _is(accepted, T.i32, (B,)):
+        _refuse(accepted, "accepted", T.i32, (B,))
     if n_draft is not None:
-        _ints(n_draft, "n_draft", "int32", (B,))
-    _dev(workspace, "workspace", torch.uint8)
-    _check(_lib.pn_verify(kind, p.data_ptr(), ps, _ptr(q) if K else 0, qs, draft.data_ptr(), _ptr(n_draft),
+        if not _is(n_draft, T.i32, (B,)):
+            _refuse(n_draft, "n_draft", T.i32, (B,))
+        n_at = n_draft.data_ptr()
+    _dev(workspace, "workspace", T.u8)
+    _check(_lib.pn_verify(kind, p.data_ptr(), p_row, q_at, q_row, draft.data_ptr(), n_at,
                           u_accept.data_ptr(), u_sample.data_ptr(), B, K, V, tokens.data_ptr(),
                           accepted.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                          _stream(stream)), "pn_verify")
+                          _handle(stream, T)), "pn_verify")

@@ -61,18 +61,32 @@ __device__ __forceinline__ int drafts_of(const VerifyArgs &A, int64_t b)
     return A.n_draft ? min(max(A.n_draft[b], 0), A.K) : A.K;
 }
 
-// Sum over the workgroup's 256 threads, in every thread.
-__device__ __forceinline__ double group_sum(double v, double *lds)
+// v of another lane by a DPP move (0 where the move has no source).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v += __shfl_xor(v, o, 64);
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-    __syncthreads();
+    const uint2 w = __builtin_bit_cast(uint2, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w.x, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w.y, CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, make_uint2(lo, hi));
+}
+// The sum over this lane and those below it in the wave: within rows of 16 lanes, then the last lane of
+// the row before into odd rows, then of the first half into the second.
+__device__ __forceinline__ double wave_scan(double v)
+{
+    v += moved<0x111, 0xF>(v);  // row_shr 1
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);  // row_bcast 15
+    v += moved<0x143, 0xC>(v);  // row_bcast 31
     return v;
+}
+__device__ __forceinline__ double last_lane(double v)
+{
+    const uint2 w = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(double, make_uint2((uint32_t)__builtin_amdgcn_readlane((int)w.x, 63),
+                                                 (uint32_t)__builtin_amdgcn_readlane((int)w.y, 63)));
 }
 
 template <int T>
@@ -81,7 +95,7 @@ __global__ void __launch_bounds__(256) verify_sums(VerifyArgs A)
     typedef typename Elem<T>::type E;
     constexpr int VEC = 16 / sizeof(E);
     typedef E EV __attribute__((ext_vector_type(VEC)));
-    __shared__ double lds[4];
+    __shared__ double2 lds[4];
     const int64_t b = blockIdx.x / (unsigned)A.chunks;
     const int chunk = (int)(blockIdx.x - b * A.chunks);
     const int lane = threadIdx.x & 63;
@@ -141,58 +155,54 @@ __global__ void __launch_bounds__(256) verify_sums(VerifyArgs A)
             sp += positive(pt);
         }
     }
-    sr = group_sum(sr, lds);
-    sp = group_sum(sp, lds);
+    sr = wave_scan(sr);
+    sp = wave_scan(sp);
+    if (lane == 63)
+        lds[threadIdx.x >> 6] = make_double2(sr, sp);
+    __syncthreads();
     if (threadIdx.x == 0)
-        A.sums[blockIdx.x] = make_double2(sr, sp);
+        A.sums[blockIdx.x] = make_double2((lds[0].x + lds[1].x) + (lds[2].x + lds[3].x),
+                                          (lds[0].y + lds[1].y) + (lds[2].y + lds[3].y));
 }
 
-// The sum of the threads before this one, and all of them; lds[0..3] is scratch.
-__device__ __forceinline__ double before(double v, double *lds, double &all)
+// Where a running sum over the workgroup's threads first passes a value: each thread tells the first of
+// its own places that does (INT32_MAX: none) with the sum before it, and the last place that has
+// anything (-1: none). `lds` is used once a kernel.
+struct Found {
+    int first, last;
+    double before;
+};
+__device__ __forceinline__ Found find(int first, int last, double before, Found *lds)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double s = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double t = __shfl_up(s, o, 64);
-        if (lane >= o)
-            s += t;
+    const unsigned long long any = __ballot(first != INT32_MAX), has = __ballot(last >= 0);
+    // the threads' places rise with the lanes
+    if (any ? lane == __ffsll(any) - 1 : lane == 0) {
+        lds[wave].first = first;
+        lds[wave].before = before;
     }
-    if (lane == 63)
-        lds[wave] = s;
+    if (has ? lane == 63 - __clzll(has) : lane == 0)
+        lds[wave].last = last;
     __syncthreads();
-    double base = 0.0;
+    Found f = lds[0];
 #pragma unroll
-    for (int w = 0; w < 3; w++)
-        if (w < wave)
-            base += lds[w];
-    all = ((lds[0] + lds[1]) + lds[2]) + lds[3];
-    __syncthreads();
-    const double prev = __shfl_up(s, 1, 64);
-    return base + (lane ? prev : 0.0);
-}
-
-// The least (or greatest) of the workgroup's values.
-__device__ __forceinline__ int group_least(int v, int *lds)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v = min(v, __shfl_xor(v, o, 64));
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = min(min(lds[0], lds[1]), min(lds[2], lds[3]));
-    __syncthreads();
-    return v;
+    for (int w = 1; w < 4; w++) {
+        if (f.first == INT32_MAX) {
+            f.first = lds[w].first;
+            f.before = lds[w].before;
+        }
+        f.last = max(f.last, lds[w].last);
+    }
+    return f;
 }
 
 template <int T>
 __global__ void __launch_bounds__(256) verify_choose(VerifyArgs A)
 {
-    __shared__ double lds[4];
-    __shared__ int least[4];
-    __shared__ double run[kChunk];
-    __shared__ double chosen_before;
+    __shared__ double2 wsum[4];
+    __shared__ double wmine[4];
+    __shared__ Found lds[2][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t b = blockIdx.x;
     const int n = drafts_of(A, b), a = A.accepted[b];
     const double2 *const sums = A.sums + b * A.chunks;
@@ -202,21 +212,32 @@ __global__ void __launch_bounds__(256) verify_choose(VerifyArgs A)
     const int c0 = min(A.chunks, (int)threadIdx.x * each), c1 = min(A.chunks, c0 + each);
     double r = 0.0, p = 0.0;
     for (int c = c0; c < c1; c++) {
-        r += sums[c].x;
-        p += sums[c].y;
+        const double2 s = sums[c];
+        r += s.x;
+        p += s.y;
     }
-    double all_r, all_p;
-    const double before_r = before(r, lds, all_r), before_p = before(p, lds, all_p);
+    const double scan_r = wave_scan(r), scan_p = wave_scan(p);
+    if (lane == 63)
+        wsum[wave] = make_double2(scan_r, scan_p);
+    __syncthreads();
+    const double all_r = (wsum[0].x + wsum[1].x) + (wsum[2].x + wsum[3].x);
     const bool whole = !(all_r > 0.0);  // r is zero everywhere: draw from p
-    const double total = whole ? all_p : all_r;
+    double total = 0.0, sum = whole ? scan_p - p : scan_r - r;
+#pragma unroll
+    for (int w = 0; w < 4; w++) {
+        const double s = whole ? wsum[w].y : wsum[w].x;
+        if (w < wave)
+            sum += s;
+        total += s;
+    }
     int64_t token = -1;
     if (total > 0.0) {
         const double at = (double)A.u_sample[b] * total;
         // the first chunk that passes `at`; if none, the last that has anything
-        double sum = whole ? before_p : before_r, found = 0.0;
+        double found = 0.0;
         int first = INT32_MAX, last = -1;
         for (int c = c0; c < c1; c++) {
-            const double s = whole ? sums[c].y : sums[c].x;
+            const double s = each == 1 ? (whole ? p : r) : whole ? sums[c].y : sums[c].x;
             if (s > 0.0) {
                 last = c;
                 if (first == INT32_MAX && sum + s > at) {
@@ -226,50 +247,49 @@ __global__ void __launch_bounds__(256) verify_choose(VerifyArgs A)
             }
             sum += s;
         }
-        int chunk = group_least(first, least);
-        const bool passed = chunk != INT32_MAX;
-        if (!passed)
-            chunk = -group_least(-last, least);
-        if (passed && first == chunk)
-            chosen_before = found;
+        const Found chunk = find(first, last, found, lds[0]);
+        const bool passed = chunk.first != INT32_MAX;
+        const int64_t base = (int64_t)(passed ? chunk.first : chunk.last) * kChunk;
 
+        // the chunk's numbers, kPer in a row a thread
         const Draw d = draw_of(A, b, a, n);
-        const int64_t base = (int64_t)chunk * kChunk;
-        for (int k = threadIdx.x; k < kChunk; k += 256) {
-            const int64_t t = base + k;
-            double v = 0.0;
+        double x[kPer], mine = 0.0;
+#pragma unroll
+        for (int k = 0; k < kPer; k++) {
+            const int64_t t = base + threadIdx.x * kPer + k;
+            x[k] = 0.0;
             if (t < A.V) {
                 const double pt = prob<T>(A.p, d.p_row + t);
-                if (whole)
-                    v = positive(pt);
-                else if (t != d.out)
-                    v = rest(pt, d.q_row < 0 ? 0.0 : prob<T>(A.q, d.q_row + t));
+                const double qt = d.q_row < 0 ? 0.0 : prob<T>(A.q, d.q_row + t);
+                x[k] = whole ? positive(pt) : t == d.out ? 0.0 : rest(pt, qt);
             }
-            run[k] = v;
         }
-        __syncthreads();
-        double mine = 0.0, all;
 #pragma unroll
         for (int k = 0; k < kPer; k++)
-            mine += run[threadIdx.x * kPer + k];
-        sum = before(mine, lds, all) + (passed ? chosen_before : 0.0);
+            mine += x[k];
+        const double scan = wave_scan(mine);
+        if (lane == 63)
+            wmine[wave] = scan;
+        __syncthreads();
+        sum = (passed ? chunk.before : 0.0) + (scan - mine);
+#pragma unroll
+        for (int w = 0; w < 3; w++)
+            if (w < wave)
+                sum += wmine[w];
         first = INT32_MAX;
         last = -1;
 #pragma unroll
         for (int k = 0; k < kPer; k++) {
             const int t = threadIdx.x * kPer + k;
-            const double v = run[t];
-            sum += v;
-            if (v > 0.0) {
+            sum += x[k];
+            if (x[k] > 0.0) {
                 last = t;
                 if (passed && first == INT32_MAX && sum > at)
                     first = t;
             }
         }
-        int t = group_least(first, least);
-        if (t == INT32_MAX)
-            t = -group_least(-last, least);
-        token = base + t;
+        const Found place = find(first, last, 0.0, lds[1]);
+        token = base + (place.first != INT32_MAX ? place.first : place.last);
     }
     if (threadIdx.x == 0)
         A.tokens[b * (A.K + 1) + a] = (int32_t)token;
