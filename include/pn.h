@@ -304,7 +304,7 @@ int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t
  * parts each (2^-16 relative at most; an fp16 q exactly).
  * Deterministic: a row's value depends on the call's shapes and its own data only.
  * workspace: pn_attend_workspace_bytes of device memory (16-byte aligned), overwritten; it may be
- * used by the next call on the same stream. */
+ * used by the next call on the same stream, calls that may overlap need one each. */
 typedef struct pn_attend_args {
     int type;                 /* PN_F32, PN_BF16 or PN_F16 */
     int B, Q, Hq;             /* Hq a multiple of cache->heads (else PN_ERR_SHAPE) */
@@ -346,7 +346,8 @@ int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *workspace,
  *      taken as 0..K
  *   tokens int32[B][K + 1]: the accepted drafts, the token after them, then -1; accepted int32[B]
  * 0 <= K <= PN_VERIFY_MAX_DRAFTS, 1 <= V < 2^30. Deterministic. The workspace is
- * pn_verify_workspace_bytes of device memory (16-byte aligned), overwritten. */
+ * pn_verify_workspace_bytes of device memory (16-byte aligned), overwritten, with any content to
+ * begin with; calls that may overlap need one each. */
 #define PN_VERIFY_MAX_DRAFTS 63
 int64_t pn_verify_workspace_bytes(int64_t B, int64_t V);
 
