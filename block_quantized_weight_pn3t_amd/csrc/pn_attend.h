@@ -1,8 +1,8 @@
 // pn_attend.h -- attention of a step's tokens over a shared prefix and each sequence's own tokens,
 // read from the microscaled cache, on gfx950.
 //
-// out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale * q.k_j). One pass over the tokens: a running
-// maximum m, l = sum exp(s - m) and O = sum exp(s - m) v, rescaled when m grows; partial results of
+// out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale * q.k_j). One pass over the tokens: a reference m
+// near the running maximum, l = sum exp(s - m) and O = sum exp(s - m) v, rescaled when m moves; partial results of
 // disjoint token ranges join as m = max m_i, l = sum l_i e^(m_i - m), O likewise.
 //
 // Tiles are 16 query rows (a row is one query token and head of a KV head's group; in the prefix the
@@ -25,13 +25,20 @@
 //   stream  few rows: memory bound. A wave has one tile of rows, q in LDS, and every (8 / tiles)-th
 //           record of the workgroup's token range, from memory straight to registers; at the end the
 //           waves of a row tile join through LDS.
-//   shared  the prefix under more than 64 rows: bound by conversions and the matrix instructions. All
-//           waves walk the same records, each with its own 16 to 64 rows. Converting a record once a
-//           wave would cost as much as its products, so it is converted once a workgroup: four waves
-//           take a chunk of 64 channels of K each, four of V, and put the operands into LDS, a stage
-//           ahead (two stages, one barrier a stage).
+//   shared  the prefix under more than 64 rows: bound by the matrix and vector instructions and LDS
+//           reads together. All waves walk the same records, each with its own 16 to 48 rows.
+//           Converting a record once a wave would cost as much as its products, so it is converted once
+//           a workgroup: each wave takes half a chunk of 64 channels of K and of V and puts the operands
+//           into LDS, K two stages ahead and V one (rings of three and two, one barrier a stage).
 // A workgroup's token range is one of `splits` of its sequence's (or the prefix's), and a second
 // kernel joins those.
+//
+// Measured: four query tokens of 24 heads over 130,077 of 4 x 256 channels, fp32, 8-bit codes (stream):
+// 62 us and 4.8 of joining, 4.4 TB/s of the cache where a copy reaches 4.8; the matrix unit is busy a
+// third of the time. 32 sequences of five tokens of 24 heads after 32,769 of 4 x 256, bf16, 4-bit codes
+// (shared): 145 us and 15 of joining 67 MB of partial results; the matrix unit is busy 35 % of the time,
+// the vector unit about as much, LDS a quarter; waves wait for LDS operands and at the barrier for
+// the rest.
 #pragma once
 
 #include <math.h>
@@ -380,9 +387,10 @@ struct State {
 
 // Scores of NR records to weights for RT tiles, as NT bf16 parts in the order of the V operand's tokens.
 // The weights are taken against the reference as it is; only where a lane's sum of them passes 2^12
-// (or is NaN: no reference yet) are the maximum found, the reference moved to it and the weights taken
-// again. Weights up to 2^12 lose nothing in fp32 and bf16, and most records need neither the maximum,
-// which is as many instructions as the rest, nor a rescaling.
+// (or is NaN: no reference yet) are the maximum of its row found, the row's reference moved to it and
+// the weights taken again. Weights up to 2^12 lose nothing in fp32 and bf16, and most records need
+// neither the maximum, which is as many instructions as the rest, nor a rescaling. The other rows of
+// the tile keep their references: a row's roundings do not depend on its neighbours.
 template <int NT, int NP, int NR, int RT>
 __device__ __forceinline__ void weigh(const f32x4_t (&s)[RT][NR][2], float scale, State<NP> (&st)[RT],
                                       bf16x8_t (&w)[RT][NR][NT])
@@ -432,7 +440,12 @@ __device__ __forceinline__ void weigh(const f32x4_t (&s)[RT][NR][2], float scale
                 for (int a = 0; a < 2; a++)
                     top = larger(larger(top, larger(s[rt][c][a][0], s[rt][c][a][1])),
                                  larger(s[rt][c][a][2], s[rt][c][a][3]));
+            // the rows of lanes i, i + 16, i + 32, i + 48 that are over
+            uint64_t rows = __ballot(!(sum[rt] <= 0x1p12f));
+            rows |= rows >> 32;
+            rows |= rows >> 16;
             top = larger(over_groups_max(top) * scale, -st[rt].base);
+            top = (rows >> (threadIdx.x & 15)) & 1 ? top : -st[rt].base;
             // (2^(m - top) of no reference at all: there is nothing to rescale, or it is NaN and stays so)
             const float f = st[rt].base == INFINITY ? 0.0f : __builtin_amdgcn_exp2f(-st[rt].base - top);
             st[rt].l *= f;
@@ -994,7 +1007,7 @@ struct Live {
 };
 
 // Few rows: joins the ranges of 64 channels of a row in a workgroup, thread = four channels of every
-// 16th range.
+// 16th range. Bound by its start and two dependent loads: 96 rows of 256 channels and 64 ranges 4.8 us.
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs A)
 {
@@ -1060,7 +1073,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs A)
         A.lse[row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// Many rows: a wave joins 256 / D rows, D / 4 lanes a row.
+// Many rows: a wave joins 256 / D rows, D / 4 lanes a row, eight ranges in flight. 3,840 rows of 256
+// channels and 18 ranges: 15 us, 4.7 TB/s.
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_rows_kernel(AttendArgs A)
 {
@@ -1112,7 +1126,7 @@ template <int FMT, int D, int NT, int RT>
 static int launch_attend(const AttendArgs &A, hipStream_t s)
 {
     constexpr auto kern = attend_kernel<FMT, D, NT, RT>;
-    // q operands of a stream workgroup, the joining of its waves, or a shared one's two stages
+    // q operands of a stream workgroup, the joining of its waves, or a shared one's rings (3 of K, 2 of V)
     const int tiles = std::max(A.own_tiles, RT > 0 ? 1 : A.prefix_tiles);
     const int bytes = std::max(std::max(tiles * (D / 32) * NT * 1024, kWaves * 16 * (D + 4 + 2) * 4), RT > 0 ? 5 * 16384 : 0);
     if (!lds_limit_once<kern>(160 * 1024))
@@ -1126,7 +1140,8 @@ static int launch_attend(const AttendArgs &A, hipStream_t s)
     const int st = launch_status();
     if (st != PN_OK || A.direct)
         return st;
-    // a wave a row where the rows fill the CUs with four waves each: 960 rows, 18 ranges
+    // D / 4 lanes a row where the rows alone fill the CUs with a wave each: 3,840 rows of 256 channels,
+    // 18 ranges 29 us a workgroup a row, 15 so; below, the workgroups a row have more loads in flight
     if (rows >= 1024)
         hipLaunchKernelGGL((attend_join_rows_kernel<D>), dim3((unsigned)((rows * (D / 4) + 255) / 256)),
                            dim3(256), 0, s, A);

@@ -1,6 +1,7 @@
 /*
  * pn.h -- C ABI of libpn.so: decode-step GEMV y = W.x over block-quantized weights decoded in
- * registers, on AMD Instinct MI355X (gfx950).
+ * registers, and a step's key/value cache, attention and verification of drafts, on AMD Instinct
+ * MI355X (gfx950).
  *
  * Formats:
  *   PN (pn3t, pn4t)  "PN weight format" (PNX-FORMAT-v0), sections "Types", "Block layout",
@@ -289,8 +290,8 @@ int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t
  *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q.k_j),   lse = log sum_j w_j
  * over every prefix token and the own tokens j <= lens[b] - nq + i, nq = q_lens[b] (Q where q_lens
  * is NULL). A row that sees nothing, and every row i >= nq, is zeros with lse = -infinity.
- * The prefix is computed for all sequences at once: its cache is read once per block of 64 rows
- * (fp32 and fp16 queries: 32), not once per sequence.
+ * The prefix is computed for all sequences at once: its cache is read once per block of rows of all
+ * sequences (64 rows, or 128 to 384 by dim and type where there are more), not once per sequence.
  *   q      [B][Q][Hq][dim] of `type` with strides in elements (channels contiguous)
  *   table  int32[B][table_width] (row stride table_stride), the own pages of each sequence;
  *          lens int32[B] own tokens, taken as 0..table_width * page
@@ -299,9 +300,9 @@ int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t
  * A page number outside the cache is taken as the nearest one inside it: an unspecified value,
  * no access out of bounds. Tokens past a sequence's length are not used, whatever lies there.
  * Arithmetic: products on the matrix cores with fp32 sums; cache numbers enter exactly (bf16 holds
- * them); running maxima and sums in fp32. bf16 q: the softmax weights are rounded to bf16 once
- * (2^-8 relative at most) where they meet v. fp32 and fp16 q: q and the weights enter as two bf16
- * parts each (2^-16 relative at most; an fp16 q exactly).
+ * them); maxima and sums in fp32. bf16 q: the softmax weights are rounded to bf16 once (2^-8 relative
+ * at most) where they meet v. fp16 and fp32 q: q enters exactly as two and three bf16 parts, the
+ * weights likewise (2^-16 and 2^-24 relative at most).
  * Deterministic: a row's value depends on the call's shapes and its own data only.
  * workspace: pn_attend_workspace_bytes of device memory (16-byte aligned), overwritten; it may be
  * used by the next call on the same stream, calls that may overlap need one each. */

@@ -368,3 +368,22 @@ def test_binding_refusals(env):
     bad(0, c.cache, prefix_table=kw["prefix_table"].long())
     bad(0, c.cache, q_lens=torch.zeros(3, dtype=torch.int32, device=c.dev))
     bad(0, c.cache, scale=float("nan"))
+
+
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("fmt,dim,prefix,B", [(MXFP8, 64, 700, 2), (MXFP4, 128, 700, 12), (MXFP8, 256, 0, 3)])
+def test_other_rows_do_not_change_a_row(env, type_, fmt, dim, prefix, B):
+    """A row's bits stay as they are whatever the rows beside it hold: others whose scores grow along the
+    tokens move their references, not this row's. Stream and shared workgroups of the prefix, own tokens."""
+    def grow(c, k, v):
+        k *= np.linspace(0.05, 3.0, len(k))[:, None, None].astype(np.float32)
+    c = Case(env, 920 + dim, fmt, 1, 6, dim, 64, prefix, [600 if not prefix else 50] * B, 2, type_, prefill=grow)
+    plain = c.check()
+    other = c.q.clone()
+    other[0, 1] *= 9
+    other[1:] *= -7
+    other[0, 0, 1:] *= 5
+    got = c.run(other)
+    assert not c.torch.equal(got[0][0, 1], plain[0][0, 1])
+    for new, old in zip(got, plain):
+        assert c.torch.equal(new[0, 0, 0], old[0, 0, 0])
