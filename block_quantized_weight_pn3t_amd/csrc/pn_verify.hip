@@ -2,9 +2,10 @@
 //
 // Draft i stands iff all before it do and u_i q_i(x_i) < p_i(x_i); after a accepted drafts the next
 // token is drawn from r = max(p_a - q_a, 0) (p_a after the last draft, or where r is zero) by
-// inversion: the first t with r_0 + .. + r_t > u R. Probabilities are fp32 at most, so u q is exact
-// in 64 bits, and differences and sums are taken there: their rounding (2^-53 a step) is far below
-// what separates two tokens.
+// inversion: the first t with r_0 + .. + r_t > u R. What is NaN or negative is no probability: its
+// draft falls and its token has r = 0. Probabilities are fp32 at most, so u q is exact in 64 bits, and
+// differences and sums are taken there: their rounding (2^-53 a step) is far below what separates two
+// tokens.
 //
 // Memory bound: one row of p and one of q a sequence. The rows are too long for one workgroup (a
 // single CU reads a small part of what the memory gives), so they are cut into chunks of kChunk, which
@@ -50,8 +51,8 @@ __device__ __forceinline__ double prob(const void *p, int64_t at)
     return (double)(float)reinterpret_cast<const typename Elem<T>::type *>(p)[at];
 }
 
-// r of one token (NaN and negative numbers count as 0)
-__device__ __forceinline__ double rest(double p, double q) { return p > q ? p - q : 0.0; }
+// r of one token: 0 where p or q is no probability, NaN or negative (p > q >= 0 leaves p positive)
+__device__ __forceinline__ double rest(double p, double q) { return p > q && q >= 0.0 ? p - q : 0.0; }
 __device__ __forceinline__ double positive(double p) { return p > 0.0 ? p : 0.0; }
 
 // How a sequence's next token is drawn: rows of p and q (one < 0: no row of q), and the draft that a
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(256) verify_kernel(VerifyArgs A)
         if (x >= 0 && x < A.V) {
             const double px = prob<T>(A.p, (b * (A.K + 1) + lane) * A.p_stride + x);
             const double qx = A.q ? prob<T>(A.q, (b * A.K + lane) * A.q_stride + x) : 1.0;
-            ok = (double)A.u_accept[b * A.K + lane] * qx < px;
+            ok = px >= 0.0 && qx >= 0.0 && (double)A.u_accept[b * A.K + lane] * qx < px;
         }
     }
     const int a = __ffsll((unsigned long long)~__ballot(ok)) - 1;  // n <= 63: some lane is false

@@ -338,10 +338,10 @@ int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *workspace,
  * accepted drafts comes one more token: the smallest t at which r_0 + .. + r_t > u_sample[b] * R,
  * R the sum of all r; r = max(p_a - q_a, 0), where a < n and that has a positive sum, else r = p_a.
  * With u uniform in [0, 1) the tokens are distributed as the target's.
- * Every product, difference, sum and comparison is in 64 bits. A NaN or a negative probability
- * counts as 0 in r and refuses its draft; a draft outside 0..V-1 is refused (and r = p_a where q is
- * NULL). Where no t qualifies (rounding of the last sum, u >= 1) the token is the last t with
- * r_t > 0, and -1 where r is zero everywhere.
+ * Every product, difference, sum and comparison is in 64 bits. A draft whose p or q is NaN or
+ * negative is refused, and a token whose p_a or q_a is has r_t = 0 (where r = p_a, p_a alone counts);
+ * a draft outside 0..V-1 is refused (and r = p_a where q is NULL). Where no t qualifies (rounding of
+ * the last sum, u >= 1) the token is the last t with r_t > 0, and -1 where r is zero everywhere.
  *   p  row (b, i) at element (b * (K + 1) + i) * p_stride, q at (b * K + i) * q_stride, both of
  *      `type`; draft int32[B][K]; u_accept fp32[B][K]; u_sample fp32[B]; n_draft int32[B] or NULL,
  *      taken as 0..K
