@@ -136,12 +136,15 @@ __device__ __forceinline__ void store4(int type, void *p, int64_t at, f32x4_t x)
 
 // N pieces of eight channels of q, piece i at q + at + 64 (i / 2) + 8 (i % 2), as NT bf16 parts: the value
 // rounded, then what that left, and so on: bf16 q has one part, fp16 two, fp32 three, each exact (8, 16
-// and 24 bits). All loads are begun before the first is waited for.
+// and 24 bits). A part that more follow stays within bf16's finite numbers, so the largest fp32 numbers
+// are made up exactly too, and an infinity is left whole to the last part: rounded to infinity at
+// once, either would leave NaN behind. All loads are begun before the first is waited for.
 template <int NT, int N>
 __device__ __forceinline__ void load_q(const AttendArgs &A, int64_t at, bool live, bf16x8_t (&part)[N][NT])
 {
     typedef typename Elem<NT == 1 ? PN_BF16 : NT == 2 ? PN_F16 : PN_F32>::type E;
     typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr float most = 0x1.fep127f;  // bf16's largest
     const E *const p = reinterpret_cast<const E *>(A.q) + (live ? at : 0);
     E4 x[N][2];
     if (A.q_vec) {
@@ -164,7 +167,7 @@ __device__ __forceinline__ void load_q(const AttendArgs &A, int64_t at, bool liv
             float v = live ? (float)x[i][j / 4][j % 4] * A.sign : 0.0f;
 #pragma unroll
             for (int t = 0; t < NT; t++) {
-                part[i][t][j] = (__bf16)v;
+                part[i][t][j] = (__bf16)(t + 1 < NT ? __builtin_amdgcn_fmed3f(v, -most, most) : v);
                 v -= (float)part[i][t][j];
             }
         }

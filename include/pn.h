@@ -289,7 +289,8 @@ int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t
  * hq / (Hq / heads)):
  *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q.k_j),   lse = log sum_j w_j
  * over every prefix token and the own tokens j <= lens[b] - nq + i, nq = q_lens[b] (Q where q_lens
- * is NULL). A row that sees nothing, and every row i >= nq, is zeros with lse = -infinity.
+ * is NULL). A row that sees nothing, and every row i >= nq, is zeros with lse = -infinity; so is one
+ * whose every score is -infinity (an infinite q). A score of +infinity or NaN makes the row NaN.
  * The prefix is computed for all sequences at once: its cache is read once per block of rows of all
  * sequences (64 rows, or 128 to 384 by dim and type where there are more), not once per sequence.
  *   q      [B][Q][Hq][dim] of `type` with strides in elements (channels contiguous)

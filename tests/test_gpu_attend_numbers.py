@@ -1,0 +1,110 @@
+"""What attention makes of single numbers: infinite, huge and NaN queries, and the bits that a query keeps
+on its way through the bf16 products.
+
+Three ways through the kernels: own tokens, a prefix under few rows, a prefix under more than 64 rows."""
+import numpy as np
+import pytest
+
+from step_reference import MXFP4, MXFP8
+from test_gpu_attend import Case, env  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = ["float32", "bfloat16", "float16"]
+WAYS = {  # prefix given the tokens, own lengths, B, Q, query heads of the one KV head
+    "own": (False, 2, 3, 8),
+    "prefix": (True, 2, 3, 8),
+    "shared": (True, 5, 4, 4),
+    "shared, more rows": (True, 15, 4, 8),
+}
+
+
+def case(env, seed, way, tokens, type_, fmt, dim, prefill, **more):
+    """Every query token sees all `tokens` tokens: with a prefix no own ones, else own ones and nq = 1 or
+    what is asked for."""
+    prefix, B, Q, G = WAYS[way]
+    if prefix:
+        return Case(env, seed, fmt, 1, G, dim, 32, tokens, [0] * B, Q, type_, prefill=prefill, **more)
+    return Case(env, seed, fmt, 1, Q * G, dim, 32, 0, [tokens] * B, 1, type_, prefill=prefill, **more)
+
+
+def put(c, q):
+    """q [B][Q][Hq][dim], as the case's queries."""
+    q = c.torch.from_numpy(q.astype(np.float32)).to(c.dtype)
+    c.q64, c.q = q.double().numpy(), q.to(c.dev)
+
+
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_infinite_queries(env, type_, way, dim):
+    """By the channel's keys: all positive, of both signs, zero in one token. A score of +infinity leaves
+    the mean undefined (NaN, log of the sum +infinity), NaN too; a row whose every score is -infinity has
+    no weight anywhere, as one that sees nothing. The other rows keep their bits."""
+    def keys(c, k, v):
+        k[:, 0, 1] = np.abs(k[:, 0, 1]) + 1.0
+        k[0, 0, 2], k[1, 0, 2] = 2.0, -2.0
+        k[:, 0, 3] = np.abs(k[:, 0, 3]) + 1.0
+        k[2, 0, 3] = 0.0
+    c = case(env, 60 + dim, way, 40, type_, MXFP8, dim, keys)
+    plain = c.run()
+    q, inf, nan = c.q64.copy(), np.inf, np.nan
+    rows = q.reshape(-1, dim)
+    want = {0: (1, inf, nan, inf), 3: (1, -inf, 0.0, -inf), 4: (2, inf, nan, inf), 9: (2, -inf, nan, inf),
+            13: (3, inf, nan, nan), 14: (3, -inf, nan, nan), 20: (5, nan, nan, nan), len(rows) - 1: (1, -inf, 0.0, -inf)}
+    for r, (channel, x, _, _) in want.items():
+        rows[r, channel] = x
+    put(c, q)
+    out, lse = c.run()
+    out, lse = out.double().numpy().reshape(-1, dim), lse.double().numpy().ravel()
+    for r, (_, _, o, l) in want.items():
+        assert np.array_equal(out[r], np.full(dim, o), equal_nan=True), (r, out[r][:8], o)
+        assert np.array_equal(lse[r], l, equal_nan=True), (r, lse[r], l)
+    others = np.setdiff1d(np.arange(len(rows)), list(want))
+    assert np.array_equal(out[others], plain[0].double().numpy().reshape(-1, dim)[others])
+    assert np.array_equal(lse[others], plain[1].double().numpy().ravel()[others])
+
+
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("fmt,dim", [(MXFP8, 64), (MXFP4, 128), (MXFP8, 256)])
+def test_a_query_keeps_its_bits(env, type_, way, fmt, dim):
+    """One token with a key of one in one channel: the log of the sum is the score, scale * q, itself. q
+    enters in parts that make it up, and products with 1 and 0 and their sums are exact. Then the score
+    times scale * log2(e) (two constants and a product: 3 u), the same less itself to the exponential and
+    back (u of it, 4 u from 2^x and log2), one sum and ln 2 (3 u): within 8 u of |scale q| + 1."""
+    def keys(c, k, v):
+        k[:], v[:] = 0.0, 1.0
+        k[:, :, 0] = 1.0
+    c = case(env, 70, way, 1, type_, fmt, dim, keys, scale=0.125)
+    rng = np.random.default_rng(71)
+    q = np.zeros(c.q64.shape)
+    q[..., 0] = rng.normal(size=q.shape[:-1]) * np.exp2(rng.integers(-6, 8, size=q.shape[:-1]))
+    put(c, q)
+    out, lse = c.run()
+    want = 0.125 * c.q64[..., 0]
+    off = np.abs(lse.double().numpy() - want) / (8 * U * (np.abs(want) + 1))
+    assert off.max() <= 1, off.max()
+    assert (out.double().numpy() == 1.0).all()
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_the_largest_queries(env, way, dim):
+    """q up to the largest fp32 number, which no bf16 part can hold alone, over keys that small: finite
+    scores, within the bound of the test before."""
+    def keys(c, k, v):
+        k[:], v[:] = 0.0, 1.0
+        k[:, :, 1] = 2.0 ** -117
+    c = case(env, 72, way, 1, "float32", MXFP8, dim, keys, scale=2.0 ** -4)
+    top = np.float64(np.finfo(np.float32).max)
+    q = np.zeros(c.q64.shape)
+    n = q[..., 0].size
+    q[..., 1] = (top * np.linspace(0.99, 1.0, n) * np.where(np.arange(n) % 2, 1, -1)).reshape(q.shape[:-1])
+    put(c, q)
+    out, lse = c.run()
+    want = 2.0 ** -121 * c.q64[..., 1]
+    off = np.abs(lse.double().numpy() - want) / (8 * U * (np.abs(want) + 1))
+    assert off.max() <= 1, off.max()
+    assert (out.numpy() == 1.0).all()
