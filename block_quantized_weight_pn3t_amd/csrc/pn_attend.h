@@ -523,11 +523,17 @@ constexpr int kWaves = 8;
 
 // A stream workgroup: rows [row0, row0 + 16 tiles) of KV head h over range `split` of a sequence's own
 // tokens (OWN) or of the prefix. Wave w has row tile w % tiles and every (8 / tiles)-th record.
+// The weights are NW bf16 parts where they meet V: three and two for fp32 and fp16 q, which lose nothing
+// that the type keeps, and two for bf16 q as well, so that its output is off by its own rounding alone.
+// A second product hides behind the memory here: 4 query tokens of 24 heads over 130,077 of 4 x 256 62.9
+// us with one part and 63.3 with two, 16 sequences of 4,096 of 8 x 128 32.2 and 32.3, 32 ragged ones of
+// 4 tokens and 96 heads of 64 42.5 and 44.8; the error against 64 bits 2.3e-3 and 1.7e-3, where rounding
+// the output makes 1.7e-3.
 template <int FMT, int D, int NT, bool OWN>
 __device__ __forceinline__ void attend_stream(const AttendArgs &A, int split, int b0, int h, int row0, int tiles,
                                               uint4 *lds)
 {
-    constexpr int NP = Rec<FMT, D>::NP;
+    constexpr int NP = Rec<FMT, D>::NP, NW = NT == 1 ? 2 : NT;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int tile = wave & (tiles - 1), streams = kWaves / tiles, stream = wave / tiles;
@@ -656,8 +662,8 @@ __device__ __forceinline__ void attend_stream(const AttendArgs &A, int split, in
             }
         }
 
-        bf16x8_t w[1][1][NT];
-        weigh<NT, NP, 1, 1>(s, A.scale, state, w);
+        bf16x8_t w[1][1][NW];
+        weigh<NW, NP, 1, 1>(s, A.scale, state, w);
         if (nan_hidden) {
 #pragma unroll
             for (int p = 0; p < NP; p++)
@@ -670,7 +676,7 @@ __device__ __forceinline__ void attend_stream(const AttendArgs &A, int split, in
 #pragma unroll
             for (int n = 0; n < 4; n++)
 #pragma unroll
-                for (int e = 0; e < NT; e++)
+                for (int e = 0; e < NW; e++)
                     st.O[p][n] = mfma(vf[n], w[0][0][e], st.O[p][n]);
         }
         if (more)
@@ -788,6 +794,10 @@ struct ReadAhead {
 // One barrier a stage: while stage t is used, K of t + 2 and V of t + 1 are written. K(t + 2) takes the
 // place of K(t - 1) and V(t + 1) that of V(t - 1), last read before the barrier that ended t - 1; the
 // reads of K(t + 1) begin before the barrier that ends t.
+// bf16 q's weights meet V rounded to bf16 once (2^-8 at most): a second part costs what the matrix unit
+// has least of. 16 sequences after 16,384 of 8 x 128, 8-bit codes 26.0 us with one part and 28.3 with
+// two, 32 of five tokens after 32,769 of 4 x 256, 4-bit codes 159 and 215; the error against 64 bits
+// 2.4e-3 and 1.7e-3, where rounding the output makes 1.7e-3. (fp32 q takes the same calls without it.)
 // (Holding waves 4-7 half a stage behind waves 0-3, so that one wave of a SIMD has the matrix unit while
 // the other converts and weighs, took four barriers a stage and came out even.)
 template <int FMT, int D, int NT, int RT>

@@ -301,9 +301,10 @@ int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t
  * A page number outside the cache is taken as the nearest one inside it: an unspecified value,
  * no access out of bounds. Tokens past a sequence's length are not used, whatever lies there.
  * Arithmetic: products on the matrix cores with fp32 sums; cache numbers enter exactly (bf16 holds
- * them); maxima and sums in fp32. bf16 q: the softmax weights are rounded to bf16 once (2^-8 relative
- * at most) where they meet v. fp16 and fp32 q: q enters exactly as two and three bf16 parts, the
- * weights likewise (2^-16 and 2^-24 relative at most).
+ * them); maxima and sums in fp32. q enters exactly, fp16 as two bf16 parts and fp32 as three. The
+ * softmax weights meet v as three parts for fp32 q (2^-24 relative at most) and as two (2^-16) for
+ * fp16 and bf16 q; a prefix under more than 64 rows of a KV head (B * Q * Hq / heads) takes those of
+ * bf16 q rounded to bf16 once (2^-8). An output is rounded to its type once.
  * Deterministic: a row's value depends on the call's shapes and its own data only.
  * workspace: pn_attend_workspace_bytes of device memory (16-byte aligned), overwritten; it may be
  * used by the next call on the same stream, calls that may overlap need one each. */

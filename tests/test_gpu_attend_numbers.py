@@ -1,5 +1,5 @@
-"""What attention makes of single numbers: infinite, huge and NaN queries, and the bits that a query keeps
-on its way through the bf16 products.
+"""What attention makes of single numbers: infinite, huge and NaN queries, and the bits that a query and a
+softmax weight keep on their way through the bf16 products.
 
 Three ways through the kernels: own tokens, a prefix under few rows, a prefix under more than 64 rows."""
 import numpy as np
@@ -11,6 +11,7 @@ from test_gpu_attend import Case, env  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
+HALF = {"float32": U, "bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}  # half a step, relative to a binade's start
 TYPES = ["float32", "bfloat16", "float16"]
 WAYS = {  # prefix given the tokens, own lengths, B, Q, query heads of the one KV head
     "own": (False, 2, 3, 8),
@@ -66,6 +67,14 @@ def test_infinite_queries(env, type_, way, dim):
     assert np.array_equal(lse[others], plain[1].double().numpy().ravel()[others])
 
 
+def one_key(c, k, v):
+    """Token 0 of a sequence (or of the prefix) has a key of zeros and a value of zeros, token 1 a key of one
+    in channel 0 and a value of ones."""
+    k[:], v[:] = 0.0, 0.0
+    k[1::2, :, 0] = 1.0
+    v[1::2] = 1.0
+
+
 @pytest.mark.parametrize("type_", TYPES)
 @pytest.mark.parametrize("way", WAYS)
 @pytest.mark.parametrize("fmt,dim", [(MXFP8, 64), (MXFP4, 128), (MXFP8, 256)])
@@ -108,3 +117,26 @@ def test_the_largest_queries(env, way, dim):
     off = np.abs(lse.double().numpy() - want) / (8 * U * (np.abs(want) + 1))
     assert off.max() <= 1, off.max()
     assert (out.numpy() == 1.0).all()
+
+
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("fmt,dim", [(MXFP8, 64), (MXFP4, 128), (MXFP8, 256)])
+def test_a_weight_keeps_its_bits(env, type_, way, fmt, dim):
+    """Two tokens, scores 0 and s = scale * q, values 0 and 1: the output is e^s / (1 + e^s). s is exact as
+    above; its scaling and the subtraction are off by 4 u |s| (|s| <= 6), two exponentials by 2 u each, the
+    sum, its inverse and the product by u each: 32 u together. The weights enter the product with the
+    values as three bf16 parts, which make them up, for fp32; as two (2^-16 at most) for fp16 and bf16; the
+    shared way takes bf16 queries' weights as one (2^-8). The output is rounded once."""
+    c = case(env, 73, way, 2, type_, fmt, dim, one_key, scale=0.25)
+    rng = np.random.default_rng(74)
+    q = np.zeros(c.q64.shape)
+    q[..., 0] = rng.uniform(-24, 24, size=q.shape[:-1])
+    put(c, q)
+    out, _ = c.run()
+    want = 1 / (1 + np.exp(-0.25 * c.q64[..., 0]))
+    parts = {"float32": 0.0, "float16": 2.0 ** -16, "bfloat16": 2.0 ** -8 if way.startswith("shared") else 2.0 ** -16}
+    tol = (32 * U + parts[type_]) * want
+    tol = tol + HALF[type_] * np.exp2(np.floor(np.log2(want + tol)))
+    off = np.abs(out.double().numpy() - want[..., None]) / tol[..., None]
+    assert off.max() <= 1, off.max()
