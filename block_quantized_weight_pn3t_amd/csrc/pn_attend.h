@@ -763,7 +763,9 @@ constexpr int stage_records(int D) { return D == 256 ? 1 : 2; }
 
 // Operands read from LDS AHEAD uses early: left to itself the compiler reads two, waits for both and
 // starts over, and an LDS read under load takes as long as several uses. begin() starts the first
-// reads, run() calls use(i, operand i) for the N operands at `from` (one every 64 uint4).
+// reads, run() calls use(i, operand i) for the N operands at `from` (one every 64 uint4). Three ahead,
+// also where two would keep 20 bytes a lane less in scratch: 32 sequences of five tokens after 32,769 of
+// 4 x 256, bf16, 8-bit codes 170 us with two and 167 with three.
 template <int AHEAD>
 struct ReadAhead {
     uint4 f[AHEAD];
@@ -892,8 +894,7 @@ __device__ __forceinline__ void attend_shared(const AttendArgs &A, int split, in
     ve = ve1;
     const uint8_t *vnext = krec;
     int page = recs.page(clamped(t_first + 3 * NR));
-    // (two where a third would spill: 8-bit codes, 32 rows of 256 channels, 172 us -> 162 with 32,769 tokens)
-    ReadAhead<FMT == PN_CACHE_MXFP8 && D == 256 && RT == 2 ? 2 : 3> ahead;
+    ReadAhead<3> ahead;
     __syncthreads();
 
     int kslot = 0, vslot = 0;  // rings' places of stage t0
