@@ -77,8 +77,8 @@ struct AttendArgs {
     const void *q;
     int64_t q_seq, q_tok, q_head;
     int q_vec;     // q can be loaded four elements at a time
-    float scale;   // |scale| * log2(e), at least the least normal number
-    float sign;    // -1 where scale < 0: q is negated as it is loaded
+    float scale;   // of the scores, times log2(e): positive
+    float factor;  // of q as it is loaded, for the rest of the scale: its sign, zero, a factor of two
     const int32_t *table, *lens, *q_lens, *prefix_table;
     int64_t table_stride;
     int table_width, prefix_len;
@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_q(const AttendArgs &A, int64_t at, bool liv
     for (int i = 0; i < N; i++)
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            float v = live ? (float)x[i][j / 4][j % 4] * A.sign : 0.0f;
+            float v = live ? (float)x[i][j / 4][j % 4] * A.factor : 0.0f;
 #pragma unroll
             for (int t = 0; t < NT; t++) {
                 part[i][t][j] = (__bf16)(t + 1 < NT ? __builtin_amdgcn_fmed3f(v, -most, most) : v);

@@ -135,8 +135,10 @@ extern "C" int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *w
     A.q_tok = a->q_token_stride;
     A.q_head = a->q_head_stride;
     A.q_vec = aligned(a->q, 4 * size) && ((A.q_seq | A.q_tok | A.q_head) & 3) == 0;
-    A.scale = fmaxf(fabsf(a->scale) * kLog2e, 0x1p-126f);
-    A.sign = a->scale < 0.0f ? -1.0f : 1.0f;
+    // a scale of zero and one that log2(e) would take past fp32 are made up in q, exactly
+    const float by = fabsf(a->scale), more = by > 0x1p126f ? 2.0f : 1.0f;
+    A.scale = fmaxf(by / more * kLog2e, 0x1p-126f);
+    A.factor = a->scale > 0.0f ? more : a->scale < 0.0f ? -more : 0.0f;
     A.table = a->table;
     A.table_stride = a->table_stride;
     A.table_width = a->table_width;

@@ -140,3 +140,41 @@ def test_a_weight_keeps_its_bits(env, type_, way, fmt, dim):
     tol = tol + HALF[type_] * np.exp2(np.floor(np.log2(want + tol)))
     off = np.abs(out.double().numpy() - want[..., None]) / tol[..., None]
     assert off.max() <= 1, off.max()
+
+
+@pytest.mark.parametrize("type_", ["float32", "bfloat16"])
+@pytest.mark.parametrize("way", WAYS)
+def test_a_scale_of_zero_and_the_largest(env, type_, way):
+    """Scores of q.k up to 1e38 under a scale of zero weigh alike, whatever q; and a scale up to the largest
+    fp32 number gives finite scores of queries that small. One bound as above: 0 and s are exact."""
+    def keys(c, k, v):
+        one_key(c, k, v)
+        k[:, :, 0] *= 2.0 ** 60
+    c = case(env, 75, way, 2, type_, MXFP8, 64, keys, scale=0.0)
+    q = np.zeros(c.q64.shape)
+    q[..., 0] = np.linspace(-1, 1, q[..., 0].size).reshape(q.shape[:-1]) * 2.0 ** 66
+    put(c, q)
+    out, lse = c.run()
+    assert (out.double().numpy() == 0.5).all()
+    assert np.abs(lse.double().numpy() - np.log(2)).max() <= 8 * U
+
+    def zeros(c, k, v):
+        k[:] = 0.0
+    for scale in (2.0 ** 127, float(np.finfo(np.float32).max), -2.0 ** 127.5):
+        c = case(env, 76, way, 1, type_, MXFP8, 64, zeros, scale=float(np.float32(scale)))
+        _, lse = c.run()
+        assert (lse.double().numpy() == 0.0).all()
+
+        def small(c, k, v):
+            k[:], v[:] = 0.0, 1.0
+            k[:, :, 0] = 2.0 ** -60
+        c = case(env, 77, way, 1, type_, MXFP8, 64, small, scale=float(np.float32(scale)))
+        q = np.zeros(c.q64.shape)
+        q[..., 0] = np.linspace(-1, 1, q[..., 0].size).reshape(q.shape[:-1]) * 2.0 ** -65
+        put(c, q)
+        out, lse = c.run()
+        want = np.float64(np.float32(scale)) * 2.0 ** -60 * c.q64[..., 0]
+        assert np.abs(want).max() >= 4
+        off = np.abs(lse.double().numpy() - want) / (8 * U * (np.abs(want) + 1))
+        assert off.max() <= 1, off.max()
+        assert (out.double().numpy() == 1.0).all()
