@@ -178,3 +178,42 @@ def test_a_scale_of_zero_and_the_largest(env, type_, way):
         off = np.abs(lse.double().numpy() - want) / (8 * U * (np.abs(want) + 1))
         assert off.max() <= 1, off.max()
         assert (out.double().numpy() == 1.0).all()
+
+
+@pytest.mark.parametrize("type_", ["float32", "float16"])
+@pytest.mark.parametrize("way", ["own", "prefix"])
+@pytest.mark.parametrize("fmt,dim", [(MXFP8, 128), (MXFP4, 256)])
+def test_small_parts_of_a_score_add_up(env, type_, way, fmt, dim):
+    """A score of one large product and of pairs 1 + d, -1 whose second parts d each 32 channels' product
+    adds: less than half a step of the large one each time, one or two whole steps together. Against a
+    key without the pairs the weights differ by e^(scale * their sum). Every sum is exact if the small
+    parts meet each other first; then the exponents are off by their own rounding alone, below 32 u."""
+    big, k0, d, scale = (2.0 ** 9, 1.0, 2.0 ** -19, 2.0 ** 13) if type_ == "float32" else (
+        2.0 ** 15, 4.0, 2.0 ** -10, 2.0 ** 5)
+    pairs = 1024 // dim if type_ == "float32" else 4  # of the 16 that 32 channels of one product hold
+
+    def keys(c, k, v):
+        k[:], v[:] = 0.0, 0.0
+        k[0::2] = 1.0
+        v[0::2] = 1.0
+        k[:, :, 0] = k0
+        k[:, :, 1] = 0.0
+    c = case(env, 78, way, 2, type_, fmt, dim, keys, scale=scale)
+    q = np.zeros(c.q64.shape)
+    for p in range(dim // 64):
+        for j in range(2):  # channels 64p + 16g + 8j + 0..7 are one product's
+            for n in range(pairs):
+                at = 64 * p + 16 * (n % 4) + 8 * j + 2 + 2 * (n // 4)
+                q[..., at], q[..., at + 1] = 1.0 + d, -1.0
+    q[..., 0] = big
+    put(c, q)
+    assert np.array_equal(c.q64, q)
+    total = dim // 32 * pairs * d
+    step = 2.0 ** -23 * big * k0
+    assert pairs * d < step / 2 and total % step == 0 and total >= step
+    out, _ = c.run()
+    want = 1 / (1 + np.exp(-scale * total))
+    tol = 32 * U * want + HALF[type_] * np.exp2(np.floor(np.log2(want)))
+    assert 0.55 < want < 0.95
+    off = np.abs(out.double().numpy() - want) / tol
+    assert off.max() <= 1, off.max()
