@@ -36,9 +36,11 @@
 // Measured: four query tokens of 24 heads over 130,077 of 4 x 256 channels, fp32, 8-bit codes (stream):
 // 62 us and 4.8 of joining, 4.4 TB/s of the cache where a copy reaches 4.8; the matrix unit is busy a
 // third of the time. 32 sequences of five tokens of 24 heads after 32,769 of 4 x 256, bf16, 4-bit codes
-// (shared): 145 us and 15 of joining 67 MB of partial results; the matrix unit is busy 35 % of the time,
-// the vector unit about as much, LDS a quarter; waves wait for LDS operands and at the barrier for
-// the rest.
+// (shared): 161 us a call among others, 15 of them the joining of 67 MB of partial results (traced,
+// each kernel by itself, 158 to 165 and 15); the matrix unit is busy 34 % of the time, the vector unit
+// about as much, LDS a quarter; waves wait for LDS operands and at the barrier for the rest.
+// Three instances of 32 rows a wave spill: 20 bytes a lane with 256 channels, bf16 q and 4-bit codes, 32
+// with 8-bit ones, 12 with 128 channels, fp16 q and 8-bit codes.
 #pragma once
 
 #include <math.h>
@@ -1193,7 +1195,7 @@ static int launch_tiles(const AttendArgs &A, hipStream_t s)
     return launch_attend<FMT, D, NT, MOST>(A, s);
 }
 
-// Launches format FMT, one source file each. parts: of q and the weights (1, 2, 3).
+// Launches format FMT, one source file each. parts: of q (1, 2, 3).
 template <int FMT>
 int launch_format(const AttendArgs &A, int dim, int parts, hipStream_t s);
 

@@ -46,7 +46,9 @@ static Cut attend_cut(const pn_cache *cache, const pn_attend_args *a)
     const int64_t own_rows = (int64_t)a->Q * G, prefix_rows = own_rows * a->B;
     const int64_t own_records = (int64_t)a->table_width * (cache->page / kTile);
     const int64_t prefix_records = (a->prefix_len + kTile - 1) / kTile;
-    const int64_t cus = device_cus();  // a workgroup a CU fills it: 8 waves of up to 256 registers
+    // One workgroup a CU: what 256 channels (134 KB of LDS) and 32 rows a wave (over 128 registers) leave
+    // room for. Of the smaller ones two would fit; cutting for two is not measured.
+    const int64_t cus = device_cus();
     const auto stream_tiles = [](int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; };
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     t.own_tiles = stream_tiles(own_rows);

@@ -304,7 +304,9 @@ int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t
  * them); maxima and sums in fp32. q enters exactly, fp16 as two bf16 parts and fp32 as three. The
  * softmax weights meet v as three parts for fp32 q (2^-24 relative at most) and as two (2^-16) for
  * fp16 and bf16 q; a prefix under more than 64 rows of a KV head (B * Q * Hq / heads) takes those of
- * bf16 q rounded to bf16 once (2^-8). An output is rounded to its type once.
+ * bf16 q rounded to bf16 once (2^-8). An output is rounded to its type once. Weights are held relative
+ * to a number near their row's largest, at which they may reach 2^12: sums of values past some 2^100
+ * can leave fp32 where their mean would not.
  * Deterministic: a row's value depends on the call's shapes and its own data only.
  * workspace: pn_attend_workspace_bytes of device memory (16-byte aligned), overwritten; it may be
  * used by the next call on the same stream, calls that may overlap need one each. */
