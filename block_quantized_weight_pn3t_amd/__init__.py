@@ -1,6 +1,7 @@
 """Python binding of libpn.so (C ABI in include/pn.h): PN (pn3t / pn4t) and NVFP4 W4A16
 decode-step GEMV, validation, decode and quantizers, the microscaled key/value cache with the
-attention that reads it, and the verification of drafted tokens, on MI355X (gfx950).
+attention that reads it, the verification of drafted tokens, and a prompt's norm, 8-bit products, keys
+rotated into the cache and log probabilities, on MI355X (gfx950).
 
 Argument marshalling only: every step runs in the HIP kernels of libpn.so. PyTorch supplies device
 memory and the current stream. There is no CPU fallback: if the library is missing, importing
@@ -18,6 +19,8 @@ __all__ = ["PN3T", "PN4T", "PNError", "row_bytes", "validate_rows", "validate_ro
            "nvfp4_dequantize_rows", "gemv_nvfp4", "fp8row_validate_rows", "fp8row_dequantize_rows", "gemv_fp8row",
            "MXFP8", "MXFP4", "Cache", "cache_page_bytes", "cache_write", "cache_read",
            "attend_workspace_bytes", "attend", "verify_workspace_bytes", "verify",
+           "int8_quantize_rows", "add_norm", "gemm_int8_workspace_bytes", "gemm_int8", "cache_append",
+           "logprobs_workspace_bytes", "logprobs",
            "library_path", "status_string", "lib"]
 
 PN3T = 124
@@ -31,6 +34,9 @@ NOALLOC_MAX_FLOATS = 262144  # M * K limit of pn_gemv_hadamard_noalloc
 MXFP8 = 0              # cache formats
 MXFP4 = 1
 VERIFY_MAX_DRAFTS = 63
+ROW_MAX_WIDTH = 65536  # add_norm and int8_quantize_rows
+GEMM_INT8_MAX_K = 131056
+LOGPROBS_MAX_TOP = 64
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libpn.so")
@@ -63,6 +69,35 @@ class AttendArgs(C.Structure):
                 ("out", C.c_void_p), ("lse", C.c_void_p)]
 
 
+class AddNormArgs(C.Structure):
+    """pn_add_norm_args of include/pn.h."""
+    _fields_ = [("type", C.c_int), ("weight_type", C.c_int), ("rows", C.c_int64), ("K", C.c_int64),
+                ("x", C.c_void_p), ("x_stride", C.c_int64), ("residual", C.c_void_p),
+                ("residual_stride", C.c_int64), ("sum", C.c_void_p), ("sum_stride", C.c_int64),
+                ("weight", C.c_void_p), ("eps", C.c_float), ("out", C.c_void_p),
+                ("out_stride", C.c_int64), ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
+class AppendArgs(C.Structure):
+    """pn_append_args of include/pn.h."""
+    _fields_ = [("type", C.c_int), ("Hq", C.c_int), ("q", C.c_void_p), ("q_token_stride", C.c_int64),
+                ("q_head_stride", C.c_int64), ("q_out", C.c_void_p), ("q_out_token_stride", C.c_int64),
+                ("q_out_head_stride", C.c_int64), ("k", C.c_void_p), ("k_token_stride", C.c_int64),
+                ("k_head_stride", C.c_int64), ("v", C.c_void_p), ("v_token_stride", C.c_int64),
+                ("v_head_stride", C.c_int64), ("rotation", C.c_void_p), ("rows", C.c_int64),
+                ("rot", C.c_int), ("interleaved", C.c_int), ("positions", C.c_void_p),
+                ("slots", C.c_void_p), ("T", C.c_int64)]
+
+
+class LogprobsArgs(C.Structure):
+    """pn_logprobs_args of include/pn.h."""
+    _fields_ = [("type", C.c_int), ("top", C.c_int), ("R", C.c_int64), ("V", C.c_int64),
+                ("stride", C.c_int64), ("logits", C.c_void_p), ("tokens", C.c_void_p),
+                ("scale", C.c_float), ("logprob", C.c_void_p), ("rank", C.c_void_p),
+                ("entropy", C.c_void_p), ("lse", C.c_void_p), ("top_ids", C.c_void_p),
+                ("top_logprobs", C.c_void_p)]
+
+
 _SIGS = {
     "pn_row_bytes": (_I64, [_I32, _I64]),
     "pn_status_string": (C.c_char_p, [_I32]),
@@ -91,6 +126,13 @@ _SIGS = {
     "pn_verify_workspace_bytes": (_I64, [_I64, _I64]),
     "pn_verify": (_I32, [_I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P,
                          _I64, _P]),
+    "pn_int8_quantize_rows": (_I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "pn_add_norm": (_I32, [_P, _P]),
+    "pn_gemm_int8_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "pn_gemm_int8": (_I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I32, _P, _I64, _P, _I64, _P]),
+    "pn_cache_append": (_I32, [_P, _P, _P]),
+    "pn_logprobs_workspace_bytes": (_I64, [_I64, _I64, _I32]),
+    "pn_logprobs": (_I32, [_P, _P, _I64, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -341,7 +383,7 @@ class _Torch:
     @classmethod
     def load(cls):
         import torch
-        cls.i32, cls.i64, cls.u8 = torch.int32, torch.int64, torch.uint8
+        cls.i32, cls.i64, cls.u8, cls.i8 = torch.int32, torch.int64, torch.uint8, torch.int8
         cls.kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
         cls.stream = torch.cuda.current_stream
         cls.f32 = torch.float32
@@ -554,3 +596,207 @@ def verify(p, q, draft, u_accept, u_sample, tokens, accepted, workspace, n_draft
                           u_accept.data_ptr(), u_sample.data_ptr(), B, K, V, tokens.data_ptr(),
                           accepted.data_ptr(), workspace.data_ptr(), workspace.numel(),
                           _handle(stream, T)), "pn_verify")
+
+
+# ---- a prompt's norm, 8-bit products, rotated keys, log probabilities -----------------------------
+
+def _rows(t, name, dtype, rows, width):
+    """The spacing of the rows of t [rows, width], of `dtype` on the device."""
+    if t.dtype is not dtype or t.shape != (rows, width) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor of {dtype} [{rows}, {width}], got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    row, column = t.stride()
+    if column != 1 and width > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return row
+
+
+def _written_rows(t, name, dtype, rows, width):
+    """The same for rows that are written: they must not overlap."""
+    row = _rows(t, name, dtype, rows, width)
+    if rows > 1 and abs(row) < width:
+        raise ValueError(f"the rows of {name} overlap")
+    return row
+
+
+def _codes(codes, scales, rows, width, T):
+    if not _is(codes, T.i8, (rows, width)):
+        _refuse(codes, "codes", T.i8, (rows, width))
+    if not _is(scales, T.f32, (rows,)):
+        _refuse(scales, "scales", T.f32, (rows,))
+
+
+def int8_quantize_rows(x, codes, scales, stream=None):
+    """codes int8[N, K] and scales fp32[N] <- the rows of x [N, K] as 8-bit integers with one scale each
+    (pn_int8_quantize_rows): activations before gemm_int8, and its weights."""
+    T = _names()
+    kind = _elem(x, "x", T)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, K], got {tuple(x.shape)}")
+    n, k = x.shape
+    row = _rows(x, "x", x.dtype, n, k)
+    _codes(codes, scales, n, k, T)
+    _check(_lib.pn_int8_quantize_rows(kind, x.data_ptr(), row, n, k, codes.data_ptr(), scales.data_ptr(),
+                                      _handle(stream, T)), "pn_int8_quantize_rows")
+
+
+_pack_add_norm = struct.Struct("@iiqqPqPqPqPfPqPP").pack  # pn_add_norm_args
+
+
+def add_norm(x, weight, eps, out=None, codes=None, scales=None, residual=None, sum=None, stream=None):
+    """The root-mean-square norm of x (+ residual) [N, K] with weight [K] (pn_add_norm): out [N, K] <- plain
+    numbers of x's type, codes int8[N, K] and scales fp32[N] <- 8-bit rows for gemm_int8; either or both.
+    sum [N, K] <- x + residual, which the norm is of; sum and out may be x or residual themselves."""
+    T = _names()
+    kind = _elem(x, "x", T)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, K], got {tuple(x.shape)}")
+    n, k = x.shape
+    dt = x.dtype
+    x_row = _rows(x, "x", dt, n, k)
+    weight_kind = _elem(weight, "weight", T)
+    if not _is(weight, weight.dtype, (k,)):
+        _refuse(weight, "weight", weight.dtype, (k,))
+    residual_at = residual_row = sum_at = sum_row = out_at = out_row = codes_at = scales_at = 0
+    if residual is not None:
+        residual_row, residual_at = _rows(residual, "residual", dt, n, k), residual.data_ptr()
+    if sum is not None:
+        sum_row, sum_at = _written_rows(sum, "sum", dt, n, k), sum.data_ptr()
+    if out is not None:
+        out_row, out_at = _written_rows(out, "out", dt, n, k), out.data_ptr()
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales go together")
+        _codes(codes, scales, n, k, T)
+        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
+    elif out is None:
+        raise ValueError("out, or codes and scales, must be given")
+    a = _pack_add_norm(kind, weight_kind, n, k, x.data_ptr(), x_row, residual_at, residual_row, sum_at, sum_row,
+                       weight.data_ptr(), eps, out_at, out_row, codes_at, scales_at)
+    _check(_lib.pn_add_norm(a, _handle(stream, T)), "pn_add_norm")
+
+
+def gemm_int8_workspace_bytes(M, N, K):
+    """Device bytes that gemm_int8 needs for a [M, K] and w [N, K]."""
+    return int(_lib.pn_gemm_int8_workspace_bytes(M, N, K))
+
+
+def gemm_int8(a, a_scales, w, w_scales, out, workspace=None, stream=None):
+    """out [M, N] (float32, bfloat16 or float16, rows of any spacing) <- the product of a int8[M, K] and w
+    int8[N, K], rows scaled by a_scales fp32[M] and w_scales fp32[N] (pn_gemm_int8). workspace: a uint8
+    tensor of gemm_int8_workspace_bytes."""
+    T = _names()
+    kind = _elem(out, "out", T)
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"a and w must be [M, K] and [N, K], got {tuple(a.shape)} and {tuple(w.shape)}")
+    m, k = a.shape
+    n = w.shape[0]
+    if not _is(a, T.i8, (m, k)):
+        _refuse(a, "a", T.i8, (m, k))
+    if not _is(w, T.i8, (n, k)):
+        _refuse(w, "w", T.i8, (n, k))
+    if not _is(a_scales, T.f32, (m,)):
+        _refuse(a_scales, "a_scales", T.f32, (m,))
+    if not _is(w_scales, T.f32, (n,)):
+        _refuse(w_scales, "w_scales", T.f32, (n,))
+    row = _written_rows(out, "out", out.dtype, m, n)
+    work_at = work_bytes = 0
+    if workspace is not None:
+        _dev(workspace, "workspace", T.u8)
+        work_at, work_bytes = workspace.data_ptr(), workspace.numel()
+    _check(_lib.pn_gemm_int8(a.data_ptr(), a_scales.data_ptr(), m, w.data_ptr(), w_scales.data_ptr(), n, k, kind,
+                             out.data_ptr(), row, work_at, work_bytes, _handle(stream, T)), "pn_gemm_int8")
+
+
+def _heads(t, name, dtype, shape):
+    """The token and head strides of t [T, heads, dim], channels contiguous."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a device tensor of {dtype} {tuple(shape)} with contiguous channels, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.stride(0), t.stride(1)
+
+
+_pack_append = struct.Struct("@iiPqqPqqPqqPqqPqiiPPq").pack  # pn_append_args
+
+
+def cache_append(cache, k, v, slots, rotation, positions=None, q=None, q_out=None, interleaved=False, stream=None):
+    """cache_write of k and v [T, heads, dim] with k turned by its tokens' positions, and q_out <- q
+    [T, Hq, dim] turned likewise (q_out may be q) (pn_cache_append). rotation fp32 [P, rot]: the cosines and
+    sines of each position for the first rot channels of a head; positions int64[T]: a token's row of it,
+    its own number unless given. interleaved: channels (2j, 2j + 1) turn together, not (j, j + rot / 2)."""
+    T = _names()
+    kind = _elem(k, "k", T)
+    n, dt = k.shape[0], k.dtype
+    shape = (n, cache.heads, cache.dim)
+    k_token, k_head = _heads(k, "k", dt, shape)
+    v_token, v_head = _heads(v, "v", dt, shape)
+    if not _is(slots, T.i64, (n,)):
+        _refuse(slots, "slots", T.i64, (n,))
+    if rotation.dim() != 2:
+        raise ValueError(f"rotation must be [positions, rot], got {tuple(rotation.shape)}")
+    if not _is(rotation, T.f32, rotation.shape):
+        _refuse(rotation, "rotation", T.f32, rotation.shape)
+    rows, rot = rotation.shape
+    positions_at = hq = q_at = q_token = q_head = out_at = out_token = out_head = 0
+    if positions is not None:
+        if not _is(positions, T.i64, (n,)):
+            _refuse(positions, "positions", T.i64, (n,))
+        positions_at = positions.data_ptr()
+    if q is not None:
+        if q.dim() != 3 or q_out is None:
+            raise ValueError("q must be [T, Hq, dim], with q_out to go to")
+        hq = q.shape[1]
+        q_token, q_head = _heads(q, "q", dt, (n, hq, cache.dim))
+        out_token, out_head = _heads(q_out, "q_out", dt, (n, hq, cache.dim))
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    a = _pack_append(kind, hq, q_at, q_token, q_head, out_at, out_token, out_head, k.data_ptr(), k_token, k_head,
+                     v.data_ptr(), v_token, v_head, rotation.data_ptr(), rows, rot, 1 if interleaved else 0,
+                     positions_at, slots.data_ptr(), n)
+    _check(_lib.pn_cache_append(cache.ref, a, _handle(stream, T)), "pn_cache_append")
+
+
+def logprobs_workspace_bytes(R, V, top=0):
+    """Device bytes that logprobs needs for R rows over V tokens and `top` likeliest tokens."""
+    return int(_lib.pn_logprobs_workspace_bytes(R, V, top))
+
+
+_pack_logprobs = struct.Struct("@iiqqqPPfPPPPPP").pack  # pn_logprobs_args
+
+
+def logprobs(logits, tokens=None, logprob=None, workspace=None, rank=None, entropy=None, lse=None, top_ids=None,
+             top_logprobs=None, scale=1.0, stream=None):
+    """Rows of logits [R, V] as distributions (pn_logprobs). logprob fp32[R] <- the log probability of
+    tokens int32[R], rank int32[R] <- how many tokens have a larger logit, entropy fp32[R], lse fp32[R] <- the
+    log of the sum of exp(scale * logits), top_ids int32[R, top] and top_logprobs fp32[R, top] <- the likeliest
+    tokens: those of them that are given. workspace: a uint8 tensor of logprobs_workspace_bytes."""
+    T = _names()
+    kind = _elem(logits, "logits", T)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [R, V], got {tuple(logits.shape)}")
+    R, V = logits.shape
+    row = _rows(logits, "logits", logits.dtype, R, V)
+    at = []
+    for t, name, dtype in ((tokens, "tokens", T.i32), (logprob, "logprob", T.f32), (rank, "rank", T.i32),
+                           (entropy, "entropy", T.f32), (lse, "lse", T.f32)):
+        if t is not None and not _is(t, dtype, (R,)):
+            _refuse(t, name, dtype, (R,))
+        at.append(0 if t is None else t.data_ptr())
+    if tokens is None and (logprob is not None or rank is not None):
+        raise ValueError("logprob and rank need tokens")
+    top = ids_at = top_at = 0
+    if top_ids is not None or top_logprobs is not None:
+        if top_ids is None or top_logprobs is None or top_ids.dim() != 2:
+            raise ValueError("top_ids and top_logprobs must both be [R, top]")
+        top = top_ids.shape[1]
+        if not _is(top_ids, T.i32, (R, top)):
+            _refuse(top_ids, "top_ids", T.i32, (R, top))
+        if not _is(top_logprobs, T.f32, (R, top)):
+            _refuse(top_logprobs, "top_logprobs", T.f32, (R, top))
+        ids_at, top_at = top_ids.data_ptr(), top_logprobs.data_ptr()
+    work_at = work_bytes = 0
+    if workspace is not None:
+        _dev(workspace, "workspace", T.u8)
+        work_at, work_bytes = workspace.data_ptr(), workspace.numel()
+    a = _pack_logprobs(kind, top, R, V, row, logits.data_ptr(), at[0], scale, at[1], at[2], at[3], at[4], ids_at,
+                       top_at)
+    _check(_lib.pn_logprobs(a, work_at, work_bytes, _handle(stream, T)), "pn_logprobs")

@@ -43,4 +43,13 @@ template <> struct Elem<PN_F32> { typedef float type; };
 template <> struct Elem<PN_BF16> { typedef __bf16 type; };
 template <> struct Elem<PN_F16> { typedef _Float16 type; };
 
+// v in fp32, for good: left to itself the compiler rounds a double that ends in 16 bits to them directly,
+// which takes up to thirty instructions.
+__device__ __forceinline__ float to_f32(double v)
+{
+    float f = (float)v;
+    asm("" : "+v"(f));
+    return f;
+}
+
 }  // namespace pn

@@ -16,7 +16,7 @@
 // whole 256-byte runs of the record. In K, 16 channels of one token are 16 contiguous bytes and
 // neighbouring tokens' pieces are neighbours: lane = 4-channel group of the piece + 4 * token + 16 *
 // piece.
-#include "pn_cache.h"
+#include "pn_cache_put.h"
 
 namespace pn {
 
@@ -36,122 +36,6 @@ int cache_view(const pn_cache *c, CacheView &view)
     view = CacheView{(uint8_t *)c->data, c->pages, c->heads, __builtin_ctz((unsigned)c->page)};
     return PN_OK;
 }
-
-// Four consecutive elements as fp32; one load where they are aligned to 4 elements (VEC).
-template <int T, bool VEC>
-__device__ __forceinline__ f32x4_t load4(const void *base, int64_t at)
-{
-    typedef typename Elem<T>::type E;
-    typedef E E4 __attribute__((ext_vector_type(4)));
-    const E *p = reinterpret_cast<const E *>(base) + at;
-    if constexpr (VEC) {
-        const E4 v = *reinterpret_cast<const E4 *>(p);
-        return f32x4_t{(float)v.x, (float)v.y, (float)v.z, (float)v.w};
-    } else {
-        return f32x4_t{(float)p[0], (float)p[1], (float)p[2], (float)p[3]};
-    }
-}
-
-// The larger of v and v moved within each row of 16 lanes.
-template <int CTRL>
-__device__ __forceinline__ uint32_t larger_of(uint32_t v)
-{
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
-}
-
-// The largest magnitude's bits of a block of 8 lanes: those that differ in the lane bits 0, 1 and 4 (K)
-// or 2, 3 and 4 (V).
-template <bool V>
-__device__ __forceinline__ uint32_t block_top(f32x4_t x)
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float f = x[j];
-        m = max(m, __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu);
-    }
-    if constexpr (V)
-        m = larger_of<0x128>(larger_of<0x124>(m));  // row_ror 4, then 8
-    else
-        m = larger_of<0x4E>(larger_of<0xB1>(m));  // quad_perm [1,0,3,2], then [2,3,0,1]
-    const auto p = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-    return max((uint32_t)p[0], (uint32_t)p[1]);
-}
-
-template <int FMT>
-__device__ __forceinline__ int exponent_byte(uint32_t top)
-{
-    constexpr int emax = FMT == PN_CACHE_MXFP8 ? 8 : 2;
-    constexpr uint32_t most = FMT == PN_CACHE_MXFP8 ? 0x600000u : 0x400000u;
-    const int e = (int)(top >> 23);
-    return e >= 254 ? 255 : max(e - emax + ((top & 0x7FFFFFu) > most ? 1 : 0), 16);
-}
-
-// The codes of four numbers with exponent byte b, in the low 32 (8-bit) or 16 (4-bit) bits. Nothing
-// saturates: the block's largest is within the type by the choice of b.
-template <int FMT>
-__device__ __forceinline__ uint32_t encode4(f32x4_t x, int b)
-{
-    if (b == 255)
-        return 0;
-    // 2^(127 - b): b is 16..253, the power 2^111..2^-126
-    const float up = __builtin_bit_cast(float, (uint32_t)(254 - b) << 23);
-    if constexpr (FMT == PN_CACHE_MXFP8) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * up, x[1] * up, 0, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * up, x[3] * up, w, true);
-        return (uint32_t)w;
-    } else {
-        uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[0] * up, x[1] * up, 1.0f, 0);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * up, x[3] * up, 1.0f, 1);
-        return w & 0xFFFFu;
-    }
-}
-
-// Offsets inside a record. `tok` is the token's place in the record (0..31), u the 4-channel group
-// of the 64-channel chunk p.
-template <int FMT, int D>
-__device__ __forceinline__ int k_code_at(int tok, int p, int u)
-{
-    const int a = tok >> 4, i = tok & 15, g = u >> 2, e = u & 3;
-    return FMT == PN_CACHE_MXFP8 ? ((((p * 2 + a) * 4 + g) * 16 + i) * 4 + e) * 4
-                                 : ((((p * 4 + g) * 16 + i) * 2 + a) * 4 + e) * 2;
-}
-template <int FMT, int D>
-__device__ __forceinline__ int v_code_at(int tok, int p, int u)
-{
-    const int a = tok >> 4, g = (tok >> 2) & 3, t = tok & 3;
-    return Rec<FMT, D>::V + (FMT == PN_CACHE_MXFP8 ? ((((p * 2 + a) * 4 + g) * 16 + u) * 4 + t) * 4
-                                                   : ((((p * 4 + g) * 16 + u) * 2 + a) * 4 + t) * 2);
-}
-template <int FMT, int D>
-__device__ __forceinline__ int k_exp_at(int tok, int p, int half)
-{
-    return Rec<FMT, D>::KE + ((half * 16 + (tok & 15)) * Rec<FMT, D>::NP + p) * 2 + (tok >> 4);
-}
-template <int FMT, int D>
-__device__ __forceinline__ int v_exp_at(int tok, int p, int half)
-{
-    return Rec<FMT, D>::VE +
-           (((half * 4 + ((tok >> 2) & 3)) * Rec<FMT, D>::NP + p) * 2 + (tok >> 4)) * 4 + (tok & 3);
-}
-
-// The record that holds slot, head h; nullptr where the slot is not in the cache.
-template <int FMT, int D>
-__device__ __forceinline__ uint8_t *record_of(const CacheView &c, int64_t slot, int h)
-{
-    if (slot < 0 || (slot >> c.page_shift) >= c.pages)
-        return nullptr;
-    const int64_t page = slot >> c.page_shift;
-    const int tile = (int)(slot & ((1 << c.page_shift) - 1)) / kTile;
-    return c.data + (((page * c.heads + h) << (c.page_shift - 5)) + tile) * Rec<FMT, D>::BYTES;
-}
-
-constexpr int kQuads = 8;  // groups of four tokens a workgroup takes
-
-struct Plain {  // a plain tensor of keys or values, strides in elements
-    const void *p;
-    int64_t token, head;
-};
 
 template <int FMT, int D, int T, bool VEC>
 __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, Plain k, Plain v,
@@ -189,28 +73,8 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, Plain k, 
         const int kp = (int)(kslot[i] & 31), vp = (int)(vslot[i] & 31);
 #pragma unroll
         for (int p = 0; p < NP; p++) {
-            // a K block is lanes that differ in bits 0, 1 and 4; a V block in bits 2, 3 and 4
-            const int kb = exponent_byte<FMT>(block_top<false>(kx[i][p]));
-            const int vb = exponent_byte<FMT>(block_top<true>(vx[i][p]));
-            const uint32_t kw = encode4<FMT>(kx[i][p], kb), vw = encode4<FMT>(vx[i][p], vb);
-            if (krec) {
-                uint8_t *const at = krec + k_code_at<FMT, D>(kp, p, ku);
-                if constexpr (FMT == PN_CACHE_MXFP8)
-                    *reinterpret_cast<uint32_t *>(at) = kw;
-                else
-                    *reinterpret_cast<uint16_t *>(at) = (uint16_t)kw;
-                if ((ku & 7) == 0)
-                    krec[k_exp_at<FMT, D>(kp, p, ku >> 3)] = (uint8_t)kb;
-            }
-            if (vrec) {
-                uint8_t *const at = vrec + v_code_at<FMT, D>(vp, p, vu);
-                if constexpr (FMT == PN_CACHE_MXFP8)
-                    *reinterpret_cast<uint32_t *>(at) = vw;
-                else
-                    *reinterpret_cast<uint16_t *>(at) = (uint16_t)vw;
-                if ((vu & 7) == 0)
-                    vrec[v_exp_at<FMT, D>(vp, p, vu >> 3)] = (uint8_t)vb;
-            }
+            put_k<FMT, D>(krec, kp, p, ku, kx[i][p]);
+            put_v<FMT, D>(vrec, vp, p, vu, vx[i][p]);
         }
     }
 }
@@ -311,25 +175,6 @@ static int launch_read(const CacheView &c, const int64_t *slots, int64_t ntok, v
     return launch_status();
 }
 
-// Calls F::template go<FMT, D, T>() for the run-time format, dim and type (all checked before).
-template <typename F>
-static int by_kind(int fmt, int dim, int type, F f)
-{
-#define PN_KIND(FMT, D)                                                                            \
-    if (fmt == FMT && dim == D)                                                                    \
-        return type == PN_F32    ? f.template operator()<FMT, D, PN_F32>()                         \
-               : type == PN_BF16 ? f.template operator()<FMT, D, PN_BF16>()                        \
-                                 : f.template operator()<FMT, D, PN_F16>();
-    PN_KIND(PN_CACHE_MXFP8, 64)
-    PN_KIND(PN_CACHE_MXFP8, 128)
-    PN_KIND(PN_CACHE_MXFP8, 256)
-    PN_KIND(PN_CACHE_MXFP4, 64)
-    PN_KIND(PN_CACHE_MXFP4, 128)
-    PN_KIND(PN_CACHE_MXFP4, 256)
-#undef PN_KIND
-    return PN_ERR_SHAPE;
-}
-
 struct WriteCall {
     CacheView c;
     Plain k, v;
@@ -356,12 +201,6 @@ struct ReadCall {
         return launch_read<FMT, D, T>(c, slots, ntok, k, v, s);
     }
 };
-
-// Tokens of one call: its token quads and heads are counted in 32 bits.
-static bool tokens_fit(int64_t ntok, int heads)
-{
-    return ntok <= (int64_t)1 << 40 && (ntok + 3) / 4 * heads < INT32_MAX;
-}
 
 }  // namespace pn
 

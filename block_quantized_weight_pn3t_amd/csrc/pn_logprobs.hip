@@ -1,0 +1,417 @@
+// pn_logprobs.hip -- rows of logits as distributions: log probability and rank of a token, entropy, and
+// the likeliest tokens, on gfx950.
+//
+// With m a row's maximum, d = x - m, l = sum e^(s d) and t = sum e^(s d) d (s the scale): log p = s d - log l
+// and entropy = log l - s t / l, in which nothing cancels (log l >= 0 >= t). One pass: each lane keeps m, l and t
+// of what it has seen and rescales them where m moves; partial results join likewise (t' = f (t + (m - m') l),
+// f = e^(s (m - m'))).
+//
+// The likeliest tokens: a wave keeps its 64 best so far, one a lane, in falling order of a 64-bit key, the
+// logit's bits in an order of whole numbers over the token's number inverted: equal logits fall by number and
+// no two keys are equal. A batch of logits is looked at only where one passes the last that counts, which
+// after the first batches is rare (about top / n of the logits at the n-th); then each lane offers its
+// best, and few are put in one by one, many are sorted among the lanes and merged.
+//
+// Memory bound for long rows. A wave reads batches of 4 KB; a row is shared by up to 64 workgroups where
+// there are few, the last to arrive joins them (pn_arrive.h).
+#include <float.h>
+
+#include <algorithm>
+
+#include "pn_arrive.h"
+#include "pn_cache.h"
+
+namespace pn {
+
+typedef unsigned long long u64;
+
+struct LogArgs {
+    const void *logits;
+    const int32_t *tokens;
+    int64_t stride;
+    int V, top, groups, batches;
+    float scale, exp2_scale;  // of the logits; times log2(e)
+    float *logprob, *entropy, *lse, *top_logprobs;
+    int32_t *rank, *top_ids;
+    u64 number;
+    u64 *arrivals;  // [row][kLine]
+    u64 *parts;     // [row][group][2]: m and l, t and count
+    u64 *keys;      // [row][group][top]
+};
+
+// A row's (or a lane's) sums so far. m = -infinity: none. A NaN, or the difference of two infinities, stays
+// in l from where it came up.
+struct Sums {
+    float m, l, t;
+    int count;  // logits larger than the token's
+};
+
+__device__ __forceinline__ float greater(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+
+// l and t relative to `from` as they are relative to `to`.
+__device__ __forceinline__ void rescale(float &l, float &t, float from, float to, float exp2_scale)
+{
+    const float d = l > 0.0f ? from - to : 0.0f;
+    const float f = __builtin_amdgcn_exp2f(d * exp2_scale);
+    t = f > 0.0f ? f * __builtin_fmaf(d, l, t) : 0.0f;
+    l = f * l;
+}
+
+__device__ __forceinline__ Sums join(Sums a, Sums b, float exp2_scale)
+{
+    const float m = greater(a.m, b.m);
+    if (!(a.l == 0.0f))
+        rescale(a.l, a.t, a.m, m, exp2_scale);
+    if (!(b.l == 0.0f))
+        rescale(b.l, b.t, b.m, m, exp2_scale);
+    return Sums{m, a.l + b.l, a.t + b.t, a.count + b.count};
+}
+
+__device__ __forceinline__ Sums other_lane(Sums a, int mask)
+{
+    return Sums{__shfl_xor(a.m, mask, 64), __shfl_xor(a.l, mask, 64), __shfl_xor(a.t, mask, 64),
+                __shfl_xor(a.count, mask, 64)};
+}
+
+// A logit and its token as a key: larger logits first, then lower numbers; never 0.
+__device__ __forceinline__ u64 key_of(float x, int token)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);  // -0 as +0
+    return (u64)(b >> 31 ? ~b : b | 0x80000000u) << 32 | (uint32_t)~token;
+}
+__device__ __forceinline__ float logit_of(u64 key)
+{
+    const uint32_t b = (uint32_t)(key >> 32);
+    return __builtin_bit_cast(float, b >> 31 ? b & 0x7FFFFFFFu : ~b);
+}
+__device__ __forceinline__ int token_of(u64 key) { return (int)~(uint32_t)key; }
+
+__device__ __forceinline__ u64 lane_key(u64 v, int lane)
+{
+    return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// One step of a bitonic network over the lanes.
+__device__ __forceinline__ u64 exchange(u64 v, int stride, bool larger)
+{
+    const u64 o = __shfl_xor(v, stride, 64);
+    return (o > v) == larger ? o : v;
+}
+// The lanes' keys in falling order.
+__device__ __forceinline__ u64 sorted(u64 v, int lane)
+{
+#pragma unroll
+    for (int size = 2; size <= 64; size *= 2)
+#pragma unroll
+        for (int stride = size / 2; stride > 0; stride /= 2)
+            v = exchange(v, stride, ((lane & stride) == 0) == ((lane & size) == 0));
+    return v;
+}
+// The 64 largest of two lists in falling order.
+__device__ __forceinline__ u64 merged(u64 a, u64 b, int lane)
+{
+    const u64 r = __shfl(b, 63 - lane, 64);
+    u64 v = a > r ? a : r;
+#pragma unroll
+    for (int stride = 32; stride > 0; stride /= 2)
+        v = exchange(v, stride, (lane & stride) == 0);
+    return v;
+}
+// `key` put into the list (its last one falls out).
+__device__ __forceinline__ u64 inserted(u64 list, u64 key, int lane)
+{
+    const int at = __popcll(__ballot(list > key));
+    // wave_shr 1
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)list, 0x138, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(list >> 32), 0x138, 0xF, 0xF, false);
+    return lane < at ? list : lane == at ? key : ((u64)hi << 32 | lo);
+}
+
+// A lane's part of a batch: 4 loads of VEC logits.
+template <int T>
+struct Batch {
+    typedef typename Elem<T>::type E;
+    static constexpr int VEC = 16 / sizeof(E), LOADS = 4, PER = VEC * LOADS, ALL = 64 * PER;
+    typedef E EV __attribute__((ext_vector_type(VEC), aligned(sizeof(E))));  // rows of any alignment
+    EV v[LOADS];
+    // Logits from `base` on of a row of V (-infinity past its end).
+    __device__ __forceinline__ void load(const E *row, int base, int V, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) {
+            const int at = base + i * 64 * VEC;
+            if (at + 64 * VEC <= V) {
+                v[i] = *reinterpret_cast<const EV *>(row + at + lane * VEC);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; j++)
+                    v[i][j] = at + lane * VEC + j < V ? row[at + lane * VEC + j] : (E)-INFINITY;
+            }
+        }
+    }
+};
+
+// Puts what passes `thr` of a batch whose first logit of this lane is token `first` into the list.
+template <int T>
+__device__ __forceinline__ void take(const float (&x)[Batch<T>::PER], int first, int top, int lane, u64 &list, float &thr)
+{
+    constexpr int VEC = Batch<T>::VEC, PER = Batch<T>::PER;
+    uint32_t left = 0;
+#pragma unroll
+    for (int j = 0; j < PER; j++)
+        left |= x[j] > thr ? 1u << j : 0u;
+    while (__any(left != 0)) {
+        float best = -INFINITY;
+        int at = 0;
+#pragma unroll
+        for (int j = 0; j < PER; j++)
+            if ((left >> j & 1) && x[j] > best) {
+                best = x[j];
+                at = j;
+            }
+        u64 key = key_of(best, first + at / VEC * 64 * VEC + at % VEC);
+        const bool in = left != 0 && key > lane_key(list, top - 1);
+        left = in ? left & ~(1u << at) : 0;
+        u64 offers = __ballot(in);
+        if (__popcll(offers) <= 8) {
+            while (offers) {
+                const int from = __ffsll(offers) - 1;
+                offers &= offers - 1;
+                list = inserted(list, lane_key(key, from), lane);
+            }
+        } else {
+            list = merged(list, sorted(in ? key : 0, lane), lane);
+        }
+    }
+    const u64 last = lane_key(list, top - 1);
+    thr = last ? logit_of(last) : -INFINITY;
+}
+
+// A row's outputs by one wave, from its sums and its list.
+__device__ __forceinline__ void write_row(const LogArgs &A, int64_t row, Sums a, u64 list, int lane, float token_logit,
+                                          bool has_token)
+{
+    const float nan = __builtin_nanf("");
+    const bool bad = !(a.l < INFINITY);  // a NaN or +infinity
+    const float log_l = logf(a.l);
+    const auto log_p = [&](float x) { return bad || a.l == 0.0f ? nan : A.scale * (x - a.m) - log_l; };
+    if (lane == 0) {
+        if (A.logprob)
+            A.logprob[row] = has_token ? log_p(token_logit) : 0.0f;
+        if (A.rank)
+            A.rank[row] = has_token ? a.count : -1;
+        if (A.entropy)
+            A.entropy[row] = bad || a.l == 0.0f ? nan : log_l - A.scale * (a.t / a.l);
+        if (A.lse)
+            A.lse[row] = bad ? nan : a.l == 0.0f ? -INFINITY : __builtin_fmaf(A.scale, a.m, log_l);
+    }
+    if (lane < A.top) {
+        A.top_ids[row * A.top + lane] = list ? token_of(list) : -1;
+        A.top_logprobs[row * A.top + lane] = bad ? nan : list ? log_p(logit_of(list)) : -INFINITY;
+    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(256) logprobs_kernel(LogArgs A)
+{
+    typedef Batch<T> B;
+    typedef typename B::E E;
+    __shared__ Sums lds_sums[4];
+    __shared__ u64 lds_list[4][64];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = blockIdx.x / (unsigned)A.groups;
+    const int group = (int)(blockIdx.x - row * A.groups);
+    const E *const x_row = reinterpret_cast<const E *>(A.logits) + row * A.stride;
+    const int token = A.tokens ? A.tokens[row] : -1;
+    const bool has_token = token >= 0 && token < A.V;
+    const float token_logit = has_token ? (float)x_row[token] : INFINITY;
+
+    Sums a{-INFINITY, 0.0f, 0.0f, 0};
+    float ref = 0.0f;  // what l and t are relative to: m, or anything while they are zero
+    u64 list = 0;
+    float thr = A.top > 0 ? -INFINITY : INFINITY;
+    int batch = group * 4 + wave;
+    B next;
+    if (batch < A.batches)
+        next.load(x_row, batch * B::ALL, A.V, lane);
+    while (batch < A.batches) {
+        const int first = batch * B::ALL + lane * B::VEC;
+        const B now = next;
+        batch += A.groups * 4;
+        if (batch < A.batches)
+            next.load(x_row, batch * B::ALL, A.V, lane);
+        float x[B::PER];
+#pragma unroll
+        for (int j = 0; j < B::PER; j++)
+            x[j] = (float)now.v[j / B::VEC][j % B::VEC];
+        float m = x[0];
+#pragma unroll
+        for (int j = 1; j < B::PER; j++)
+            m = greater(m, x[j]);
+        if (__any(m > thr))
+            take<T>(x, first, A.top, lane, list, thr);
+        m = greater(a.m, m);
+        if (m > a.m) {
+            rescale(a.l, a.t, ref, m, A.exp2_scale);
+            a.m = ref = m;
+        }
+#pragma unroll
+        for (int j = 0; j < B::PER; j++) {
+            const float d = x[j] - ref, e = __builtin_amdgcn_exp2f(d * A.exp2_scale);
+            a.l += e;
+            a.t = __builtin_fmaf(e, greater(d, -FLT_MAX), a.t);  // nothing where e is 0 and d -infinity
+            a.count += x[j] > token_logit;
+        }
+    }
+#pragma unroll
+    for (int mask = 1; mask < 64; mask *= 2)
+        a = join(a, other_lane(a, mask), A.exp2_scale);
+
+    // the workgroup's waves into the first
+    if (lane == 0)
+        lds_sums[wave] = a;
+    lds_list[wave][lane] = list;
+    __syncthreads();
+    if (wave == 0) {
+        a = join(join(lds_sums[0], lds_sums[1], A.exp2_scale), join(lds_sums[2], lds_sums[3], A.exp2_scale), A.exp2_scale);
+        if (A.top > 0)
+            for (int w = 1; w < 4; w++)
+                list = merged(list, lds_list[w][lane], lane);
+    }
+    if (A.groups == 1) {
+        if (wave == 0)
+            write_row(A, row, a, list, lane, token_logit, has_token);
+        return;
+    }
+    if (wave == 0) {
+        const int64_t at = row * A.groups + group;
+        if (lane == 0) {
+            put_shared(A.parts + 2 * at, (u64)__builtin_bit_cast(uint32_t, a.l) << 32 | __builtin_bit_cast(uint32_t, a.m));
+            put_shared(A.parts + 2 * at + 1, (u64)(uint32_t)a.count << 32 | __builtin_bit_cast(uint32_t, a.t));
+        }
+        if (lane < A.top)
+            put_shared(A.keys + at * A.top + lane, list);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // every lane's stores
+        if (lane == 0)
+            last = arrive_last(A.arrivals + row * kLine, A.number, (unsigned)A.groups);
+    }
+    __syncthreads();
+    if (!last)
+        return;
+    // the groups' lists dealt to the waves
+    if (A.top > 0) {
+        list = 0;
+        for (int g = wave; g < A.groups; g += 4)
+            list = merged(list, lane < A.top ? get_shared(A.keys + (row * A.groups + g) * A.top + lane) : 0, lane);
+        lds_list[wave][lane] = list;
+    }
+    __syncthreads();
+    if (wave != 0)
+        return;
+    a = Sums{-INFINITY, 0.0f, 0.0f, 0};
+    if (lane < A.groups) {
+        const u64 *const p = A.parts + 2 * (row * A.groups + lane);
+        const u64 u = get_shared(p), v = get_shared(p + 1);
+        a = Sums{__builtin_bit_cast(float, (uint32_t)u), __builtin_bit_cast(float, (uint32_t)(u >> 32)),
+                 __builtin_bit_cast(float, (uint32_t)v), (int)(v >> 32)};
+    }
+#pragma unroll
+    for (int mask = 1; mask < 64; mask *= 2)
+        a = join(a, other_lane(a, mask), A.exp2_scale);
+    if (A.top > 0)
+        for (int w = 1; w < 4; w++)
+            list = merged(list, lds_list[w][lane], lane);
+    write_row(A, row, a, list, lane, token_logit, has_token);
+}
+
+// A batch has 1024 logits of four bytes or 2048 of two.
+static int log_batches(int type, int64_t V)
+{
+    const int all = type == PN_F32 ? Batch<PN_F32>::ALL : Batch<PN_BF16>::ALL;
+    return (int)((V + all - 1) / all);
+}
+
+// Workgroups of a row: enough in all to fill the memory pipe, a batch at least for each wave.
+static int log_groups(int64_t R, int batches)
+{
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (batches + 3) / 4), (1024 + R - 1) / R));
+}
+
+static bool logits_fit(int64_t R, int64_t V, int top)
+{
+    return R >= 0 && R <= INT32_MAX / 64 && V >= 1 && V < (int64_t)1 << 30 && top >= 0 && top <= PN_LOGPROBS_MAX_TOP;
+}
+
+}  // namespace pn
+
+using namespace pn;
+
+extern "C" int64_t pn_logprobs_workspace_bytes(int64_t R, int64_t V, int top)
+{
+    if (!logits_fit(R, V, top) || R == 0)
+        return 0;
+    // of the type that has more batches
+    const int groups = log_groups(R, log_batches(PN_F32, V));
+    return groups == 1 ? 0 : R * kLine * 8 + R * groups * (2 + top) * 8;
+}
+
+extern "C" int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!a)
+        return PN_ERR_NULL;
+    const int size = elem_bytes(a->type);
+    if (size == 0)
+        return PN_ERR_FORMAT;
+    if (!logits_fit(a->R, a->V, a->top) || !(a->scale > 0.0f && a->scale <= FLT_MAX))
+        return PN_ERR_SHAPE;
+    if (a->R == 0)
+        return PN_OK;
+    if (!a->logits || ((a->logprob || a->rank) && !a->tokens) || (a->top > 0 && (!a->top_ids || !a->top_logprobs)))
+        return PN_ERR_NULL;
+    if (!aligned(a->logits, size) || !aligned(a->tokens, 4) || !aligned(a->logprob, 4) || !aligned(a->rank, 4) ||
+        !aligned(a->entropy, 4) || !aligned(a->lse, 4) || !aligned(a->top_ids, 4) || !aligned(a->top_logprobs, 4))
+        return PN_ERR_ALIGN;
+    const int64_t need = pn_logprobs_workspace_bytes(a->R, a->V, a->top);
+    if (need > 0) {
+        if (!workspace)
+            return PN_ERR_NULL;
+        if (!aligned(workspace, 16))
+            return PN_ERR_ALIGN;
+        if (workspace_bytes < need)
+            return PN_ERR_WORKSPACE;
+    }
+    const int st = check_device();
+    if (st != PN_OK)
+        return st;
+    LogArgs A = {};
+    A.logits = a->logits;
+    A.tokens = a->tokens;
+    A.stride = a->stride;
+    A.V = (int)a->V;
+    A.top = a->top;
+    A.batches = log_batches(a->type, a->V);
+    A.groups = log_groups(a->R, A.batches);
+    A.scale = a->scale;
+    A.exp2_scale = (float)std::min((double)a->scale * 1.4426950408889634, (double)FLT_MAX);
+    A.logprob = a->logprob;
+    A.entropy = a->entropy;
+    A.lse = a->lse;
+    A.top_logprobs = a->top_logprobs;
+    A.rank = a->rank;
+    A.top_ids = a->top_ids;
+    A.number = call_number();
+    A.arrivals = (u64 *)workspace;
+    A.parts = A.arrivals + a->R * kLine;
+    A.keys = A.parts + a->R * A.groups * 2;
+    const dim3 grid((unsigned)(a->R * A.groups));
+    hipStream_t s = (hipStream_t)stream;
+    if (a->type == PN_F32)
+        hipLaunchKernelGGL((logprobs_kernel<PN_F32>), grid, dim3(256), 0, s, A);
+    else if (a->type == PN_BF16)
+        hipLaunchKernelGGL((logprobs_kernel<PN_BF16>), grid, dim3(256), 0, s, A);
+    else
+        hipLaunchKernelGGL((logprobs_kernel<PN_F16>), grid, dim3(256), 0, s, A);
+    return launch_status();
+}

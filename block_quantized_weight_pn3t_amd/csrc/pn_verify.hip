@@ -14,27 +14,19 @@
 // takes all its chunks' sums, finds the chunk in which the running sum passes u R and the token inside
 // it. (As two kernels 13.0 us a call for one sequence, 10.8 so.)
 //
-// Arrivals are counted in a word of the workspace, which nobody clears beforehand: its upper 44 bits
-// hold the call's number, anything else there counts as zero arrivals, and the last one to arrive
-// leaves zero, so a replayed graph finds it as the first run did. (An arrival takes about 30 ns of its
-// word's cache line, one after another: with 122 workgroups a sequence and the words of 32 sequences in
-// two lines, 148 us instead of 14. So there are few, and a line a word.) Which workgroup is last changes
-// nothing in the result. The sums are atomic stores and loads at the device's scope, as the eight
-// XCDs' caches are not kept alike within a kernel: they pass those caches by, so all that is left to
-// order is that a store is complete before the arrival is counted, by a wait, and that the loads come
-// after the last arrival, by the barrier. (A release and an acquire at the device's scope promise the
-// same in the language's terms, but the release writes the whole XCD's cache back: 32 sequences 19.5 us
-// without, 48 with.)
+// How arrivals are counted and how the sums reach the last workgroup: pn_arrive.h. (With 122 workgroups a
+// sequence and the words of 32 sequences in two cache lines 148 us instead of 14, so there are few, and a
+// line a word. With a release and an acquire instead of stores and loads at the device's scope, 32 sequences
+// 48 us instead of 19.5.)
 #include <algorithm>
-#include <atomic>
 
+#include "pn_arrive.h"
 #include "pn_cache.h"
 
 namespace pn {
 
 constexpr int kChunk = 2048;        // numbers of a row a workgroup sums
 constexpr int kPer = kChunk / 256;  // of those, a thread's
-constexpr int kLine = 16;           // words of a cache line
 
 struct VerifyArgs {
     const void *p, *q;
@@ -132,26 +124,12 @@ __device__ __forceinline__ Found find(int first, int last, double before, Found 
 
 __device__ __forceinline__ void put_sum(double2 *at, double2 v)
 {
-    __hip_atomic_store(&at->x, v.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&at->y, v.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    put_shared(&at->x, v.x);
+    put_shared(&at->y, v.y);
 }
 __device__ __forceinline__ double2 get_sum(const double2 *at)
 {
-    return make_double2(__hip_atomic_load(&at->x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
-                        __hip_atomic_load(&at->y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-}
-
-// Counts one arrival of call `number` and returns how many there were with it.
-__device__ __forceinline__ unsigned arrive(unsigned long long *word, unsigned long long number)
-{
-    constexpr unsigned long long count = (1ull << 20) - 1;
-    unsigned long long old = __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // each turn another workgroup has arrived: at most as many turns as workgroups
-    while ((old & ~count) != number)
-        if (__hip_atomic_compare_exchange_strong(word, &old, number | 1, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT))
-            return 1;
-    return (unsigned)((__hip_atomic_fetch_add(word, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1) & count);
+    return make_double2(get_shared(&at->x), get_shared(&at->y));
 }
 
 // The token after a accepted drafts of n, from all chunks' sums.
@@ -332,12 +310,8 @@ __global__ void __launch_bounds__(256) verify_kernel(VerifyArgs A)
             put_sum(A.sums + b * A.chunks + chunk, make_double2((w[0].x + w[1].x) + (w[2].x + w[3].x),
                                                                 (w[0].y + w[1].y) + (w[2].y + w[3].y)));
     }
-    if (threadIdx.x == 0) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the sums are at the device's scope
-        last = arrive(A.arrivals + b * kLine, A.number) == (unsigned)A.groups;
-        if (last)
-            __hip_atomic_store(A.arrivals + b * kLine, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    if (threadIdx.x == 0)
+        last = arrive_last(A.arrivals + b * kLine, A.number, (unsigned)A.groups);
     __syncthreads();
     if (last)
         choose<T>(A, b, n, a);
@@ -351,17 +325,6 @@ static int launch_verify(const VerifyArgs &A, int64_t B, hipStream_t s)
 }
 
 static int64_t verify_chunks(int64_t V) { return (V + kChunk - 1) / kChunk; }
-
-// A number for a call, not zero, in the upper 44 bits: no two of 2^44 calls have the same.
-static unsigned long long call_number()
-{
-    static std::atomic<unsigned long long> calls{0};
-    unsigned long long n;
-    do
-        n = (calls.fetch_add(1, std::memory_order_relaxed) * 0x9E3779B97F4A7C15ull) << 20;
-    while (n == 0);
-    return n;
-}
 
 }  // namespace pn
 

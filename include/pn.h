@@ -1,7 +1,8 @@
 /*
  * pn.h -- C ABI of libpn.so: decode-step GEMV y = W.x over block-quantized weights decoded in
- * registers, and a step's key/value cache, attention and verification of drafts, on AMD Instinct
- * MI355X (gfx950).
+ * registers; a step's key/value cache, attention and verification of drafts; and what a prompt
+ * takes beside them: the norm, products of 8-bit integers, keys rotated into the cache, log
+ * probabilities of tokens; on AMD Instinct MI355X (gfx950).
  *
  * Formats:
  *   PN (pn3t, pn4t)  "PN weight format" (PNX-FORMAT-v0), sections "Types", "Block layout",
@@ -360,6 +361,130 @@ int pn_verify(int type, const void *p, int64_t p_stride, const void *q, int64_t 
               const int32_t *draft, const int32_t *n_draft, const float *u_accept,
               const float *u_sample, int64_t B, int64_t K, int64_t V, int32_t *tokens,
               int32_t *accepted, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ---- 8-bit rows: the norm before a product, and products of them ---------------------------------
+ * A row of K numbers t as 8-bit integers with one scale: T = max |t|,
+ *   code = rint((127 * t) / T), product and quotient in 64 bits, ties to even; scale = T / 127
+ * and the row stands for code * scale. Every code is fixed by this rule. A row of zeros has codes and
+ * a scale of zero; a row with a NaN or an infinity has zero codes and a scale of NaN.
+ * 1 <= K <= PN_ROW_MAX_WIDTH (else PN_ERR_SHAPE). Rows of plain numbers may have any stride (in
+ * elements) and alignment of their element; 16-byte aligned rows with K a multiple of 8 are faster. */
+#define PN_ROW_MAX_WIDTH 65536
+
+/* x[N][K] of `type`, row n at element n * x_stride; codes int8[N][K], scales fp32[N]. */
+int pn_int8_quantize_rows(int type, const void *x, int64_t x_stride, int64_t N, int64_t K,
+                          int8_t *codes, float *scales, void *stream);
+
+/* The residual's addition and the root-mean-square norm of rows:
+ *   h = x + residual, added in fp32 and rounded to `type` (h = x without a residual), written to sum
+ *   y = h * r * weight,   r = 1 / sqrt(sum_k h_k^2 / K + eps)
+ * as plain numbers (out, rounded to fp32 and to `type`) and as 8-bit rows: codes by the rule above of
+ * t = h * weight (exact in 64 bits; r, the same for a whole row, enters the scale alone), scale =
+ * T * r / 127. out or codes may be NULL, not both; codes and scales go together. sum and out may be
+ * the memory of x or of residual (at the same stride). Sums and r in 64 bits. A row with a NaN or an infinity
+ * (after the addition, or in the weight) is what the formula gives in out, and zero codes with a scale
+ * of NaN; so is, in both, a row of zeros where eps is zero. */
+typedef struct pn_add_norm_args {
+    int type;             /* of x, residual, sum and out */
+    int weight_type;
+    int64_t rows, K;
+    const void *x;
+    int64_t x_stride;
+    const void *residual; /* may be NULL */
+    int64_t residual_stride;
+    void *sum;            /* may be NULL */
+    int64_t sum_stride;
+    const void *weight;   /* [K] */
+    float eps;            /* finite, not negative (else PN_ERR_SHAPE) */
+    void *out;
+    int64_t out_stride;
+    int8_t *codes;        /* [rows][K] */
+    float *scales;
+} pn_add_norm_args;
+
+int pn_add_norm(const pn_add_norm_args *a, void *stream);
+
+/* out[m * out_stride + n] = (sum_k a[m][k] * w[n][k]) * a_scales[m] * w_scales[n], a int8[M][K], w int8[N][K]
+ * (codes from -128 on), out of `type` (PN_F32, PN_BF16, PN_F16). The sum is exact; it is converted to
+ * fp32, multiplied by a_scales[m], then by w_scales[n] in fp32 and rounded to its type: three
+ * roundings of 2^-24 and the type's. K a positive multiple of 16, at most PN_GEMM_INT8_MAX_K (sums
+ * stay below 2^31; else PN_ERR_SHAPE); M and N any. a and w 16-byte aligned.
+ * Deterministic. workspace: pn_gemm_int8_workspace_bytes of device memory (16-byte aligned), with any
+ * content to begin with, overwritten; calls that may overlap need one each. */
+#define PN_GEMM_INT8_MAX_K 131056
+int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t *w,
+                 const float *w_scales, int64_t N, int64_t K, int type, void *out,
+                 int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ---- Rotated keys into the cache -----------------------------------------------------------------
+ * pn_cache_write of T tokens with the position rotation applied on the way: of each head's channels
+ * the first `rot` turn in pairs (a, b) by the token's row of a table of cosines and sines,
+ *   a' = a cos - b sin,  b' = a sin + b cos
+ * pair j being channels (j, j + rot / 2), or (2j, 2j + 1) where `interleaved`; the others stay. Keys are
+ * turned in 64 bits, rounded once to fp32 and then quantised as pn_cache_write does, so every bit of
+ * the cache is fixed; values are quantised as they are. Queries are turned likewise, rounded to fp32 and
+ * to their type.
+ * A token whose slot is outside the cache writes no key and no value; its queries are turned all the
+ * same. A position outside the table is taken as the nearest row inside it. */
+typedef struct pn_append_args {
+    int type;                /* of q, q_out, k and v: PN_F32, PN_BF16 or PN_F16 */
+    int Hq;                  /* query heads, 1 or more where q is given; need not be a multiple of cache->heads */
+    const void *q;           /* may be NULL: no queries */
+    int64_t q_token_stride, q_head_stride;       /* elements, channels of a head contiguous (all strides) */
+    void *q_out;             /* may be q, with its strides */
+    int64_t q_out_token_stride, q_out_head_stride;
+    const void *k;
+    int64_t k_token_stride, k_head_stride;
+    const void *v;
+    int64_t v_token_stride, v_head_stride;
+    const float *rotation;   /* fp32 [rows][rot]: rot / 2 cosines, then rot / 2 sines; 16-byte aligned */
+    int64_t rows;            /* 1 or more */
+    int rot;                 /* a positive multiple of 8, at most cache->dim (else PN_ERR_SHAPE) */
+    int interleaved;         /* 0 or 1 */
+    const int64_t *positions; /* int64[T] rows of the table; NULL: token t has row t (then rows >= T) */
+    const int64_t *slots;    /* as of pn_cache_write */
+    int64_t T;
+} pn_append_args;
+
+int pn_cache_append(const pn_cache *cache, const pn_append_args *a, void *stream);
+
+/* ---- Log probabilities of tokens -----------------------------------------------------------------
+ * R rows of V logits x (row r at element r * stride) as distributions p = exp(scale * x) / sum:
+ *   logprob[r] = log p(tokens[r]);  rank[r]: how many tokens have a larger logit
+ *   entropy[r] = -sum p log p;  lse[r] = log sum exp(scale * x)
+ *   top_ids[r][i], top_logprobs[r][i]: the `top` likeliest tokens in falling order of their logits, the
+ *   lowest number first among equals (+0 and -0 are equal), with their log probabilities
+ * Any of the outputs may be NULL (top_ids and top_logprobs only with top = 0). A token outside 0..V-1
+ * (a padding row's -1) has logprob 0 and rank -1. Tokens of logit -infinity have no part: logprob
+ * -infinity, never among the top; where fewer than `top` others are left, ids are -1 and log probabilities
+ * -infinity. A row of -infinity alone has lse -infinity, and entropy and a (valid) token's logprob NaN. A row
+ * with a NaN or +infinity has NaN in every output but rank and top_ids, which go by comparisons (a NaN
+ * is neither counted nor among the top).
+ * Maxima, exponentials and sums in fp32 relative to a row's running maximum. Deterministic.
+ * 1 <= V < 2^30, 0 <= top <= PN_LOGPROBS_MAX_TOP, scale positive and finite (else PN_ERR_SHAPE).
+ * workspace: pn_logprobs_workspace_bytes of device memory (16-byte aligned), with any content to
+ * begin with, overwritten; calls that may overlap need one each. */
+#define PN_LOGPROBS_MAX_TOP 64
+typedef struct pn_logprobs_args {
+    int type;               /* of the logits: PN_F32, PN_BF16 or PN_F16 */
+    int top;
+    int64_t R, V, stride;
+    const void *logits;
+    const int32_t *tokens;  /* may be NULL where logprob and rank are */
+    float scale;
+    float *logprob;
+    int32_t *rank;
+    float *entropy;
+    float *lse;
+    int32_t *top_ids;       /* [R][top] */
+    float *top_logprobs;    /* [R][top] */
+} pn_logprobs_args;
+
+int64_t pn_logprobs_workspace_bytes(int64_t R, int64_t V, int top);
+
+int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
