@@ -1,10 +1,24 @@
 // pn_gemm_int8.hip -- products of 8-bit integers with a scale for each row of either side, on gfx950.
 //
 // out[m][n] = (sum_k a[m][k] w[n][k]) a_scales[m] w_scales[n]: exact sums in 32 bits on the matrix cores
-// (16x16x64: 64 products a lane pair and instruction), scaled in fp32 as they are written.
+// (16x16x64 instructions, rows of w as the rows of the result, so a lane ends with four neighbouring n of one
+// m), scaled in fp32 as they are written. Integer sums have no order, so K may be cut in any way.
 //
-// A workgroup of four waves has a tile of 64 x 64 outputs, a wave 32 x 32 of it; 64 of K at a time come
-// through LDS.
+// Operands come from memory to LDS directly, 128 of K (a cache line of each row) at a time. A row's line lies in
+// LDS as eight pieces of 16 bytes, piece p of row r at place p ^ (r & 7): a load writes a wave's 1 KB in a row,
+// so the exchange is made in the addresses that it reads, and an instruction's operands of 16 rows come from
+// all banks. Past the end of K the pieces are read from 16 zero bytes instead.
+//
+// Three kernels, by the number of tokens and of tiles:
+//   stream  up to 32 tokens: memory bound, every weight read once. A workgroup has an even share of w's
+//           rows; its waves share each tile of 32 rows by K and run on their own, several loads deep, until
+//           their sums meet in LDS.
+//   tile    tiles of 64 x 64 or 128 x 128, where there are too few of the next for all CUs; K is cut among
+//           workgroups where there are too few of these, too, and the last to arrive adds up (pn_arrive.h).
+//   large   tiles of 256 x 256: matrix bound.
+#include <algorithm>
+
+#include "pn_arrive.h"
 #include "pn_cache.h"
 
 namespace pn {
@@ -17,55 +31,576 @@ struct GemmArgs {
     int64_t M, N, out_stride;
     int K;
     void *out;
+    int tiles_m, tiles_n;  // of the outputs
+    int vec;               // rows of out take stores of 16 bytes
+    int splits;            // parts of K, of `each` lines
+    int each;
+    unsigned long long number;     // of the call (pn_arrive.h)
+    unsigned long long *arrivals;  // [tile][kLine]
+    unsigned long long *parts;     // [tile][part][numbers of a thread / 2][thread]
 };
 
-template <int T>
-__global__ void __launch_bounds__(256) gemm_int8_kernel(GemmArgs A)
+// 16 bytes that stand for K past its end.
+__device__ const i32x4_t kZeros[1] = {{0, 0, 0, 0}};
+
+// 16 bytes a lane from memory to LDS, a wave's in a row from lds on. In assembly, since the compiler would have
+// every read of LDS wait for every such load.
+__device__ __forceinline__ void load_lds(const int8_t *p, uint32_t lds)
 {
-    __shared__ i32x4_t lds[2][64][5];  // rows of 64 bytes and 16 of padding
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-    const int r = threadIdx.x >> 2, c = threadIdx.x & 3;
-    const int8_t *const pa = A.a + min(m0 + r, A.M - 1) * A.K + 16 * c;
-    const int8_t *const pw = A.w + min(n0 + r, A.N - 1) * A.K + 16 * c;
-    const int i = lane & 15, g = lane >> 4, wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-    i32x4_t acc[2][2] = {};
-    for (int k = 0; k < A.K; k += 64) {
-        const bool in = k + 16 * c < A.K;
-        const i32x4_t va = in ? *reinterpret_cast<const i32x4_t *>(pa + k) : i32x4_t{0, 0, 0, 0};
-        const i32x4_t vw = in ? *reinterpret_cast<const i32x4_t *>(pw + k) : i32x4_t{0, 0, 0, 0};
-        __syncthreads();
-        lds[0][r][c] = va;
-        lds[1][r][c] = vw;
-        __syncthreads();
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+
+// An offset that is worked out where it is used, and not kept in a register for the whole loop.
+__device__ __forceinline__ uint32_t here(uint32_t offset)
+{
+    asm volatile("" : "+v"(offset));
+    return offset;
+}
+
+__device__ __forceinline__ void order() { __builtin_amdgcn_sched_barrier(0); }
+__device__ __forceinline__ void barrier()
+{
+    order();
+    __builtin_amdgcn_s_barrier();
+    order();
+}
+// Waits until at most VM loads from memory are under way and (LGKM) all of LDS's.
+template <int VM, bool LGKM>
+__device__ __forceinline__ void wait()
+{
+    static_assert(VM < 64);
+    order();
+    __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | (LGKM ? 0 : 15) << 8 | (VM >> 4) << 14);
+    order();
+}
+
+__device__ __forceinline__ i32x4_t products(i32x4_t w, i32x4_t a, i32x4_t c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a, c, 0, 0, 0);
+}
+
+// ---- up to 32 tokens ------------------------------------------------------------------------------
+
+// EIGHTS: eights of tokens that are loaded, 1, 2 or 4.
+template <int EIGHTS>
+struct Stream {
+    static constexpr int WAVES = 4, ROWS = 32, TILES = (EIGHTS + 1) / 2;  // 16 tokens a tile
+    static constexpr int STAGE = (ROWS + 8 * EIGHTS) * 128, LOADS = STAGE / 1024;
+    static constexpr int STAGES = EIGHTS == 4 ? 3 : 5;
+    static constexpr int ROW = ROWS + 4;                         // a token's sums in LDS, padded
+    static constexpr int SUMS = WAVES * TILES * 16 * ROW * 4;    // bytes; twice, for every other tile
+    static constexpr int MOST = 1024;                            // rows a workgroup has
+    static constexpr int BYTES = WAVES * STAGES * STAGE + 2 * SUMS + (MOST + 32) * 4;
+};
+
+template <int T, int EIGHTS>
+__global__ void __launch_bounds__(256) gemm_int8_stream_kernel(GemmArgs A)
+{
+    typedef Stream<EIGHTS> S;
+    typedef typename Elem<T>::type E;
+    extern __shared__ i32x4_t lds[];
+    char *const base = reinterpret_cast<char *>(lds);
+    int *const sums = reinterpret_cast<int *>(base + S::WAVES * S::STAGES * S::STAGE);
+    float *const scales = reinterpret_cast<float *>(base + S::WAVES * S::STAGES * S::STAGE + 2 * S::SUMS);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // an even share of the rows
+    const int64_t share = A.N / gridDim.x, more = A.N % gridDim.x;
+    const int64_t n0 = blockIdx.x * share + min((int64_t)blockIdx.x, more);
+    const int rows = (int)share + (blockIdx.x < more);
+    const int tiles = (rows + S::ROWS - 1) / S::ROWS, steps = ((A.K + 127) / 128 + S::WAVES - 1) / S::WAVES;
+    for (int i = threadIdx.x; i < rows; i += 256)
+        scales[i] = A.w_scales[n0 + i];
+    if (threadIdx.x < 32)
+        scales[S::MOST + threadIdx.x] = A.a_scales[min((int64_t)threadIdx.x, A.M - 1)];
+
+    const int r = lane >> 3, piece = (lane & 7) ^ r;
+    const uint32_t stages = (uint32_t)(uintptr_t)lds + wave * S::STAGES * S::STAGE;
+    // the next load: its tile's first row, its line of K and its stage
+    int next_row = 0, next_step = 0, next_stage = 0;
+    const auto load = [&]() {
+        const int k = (next_step * S::WAVES + wave) * 128 + 16 * piece;
+        const bool in = k < A.K && next_row < rows;
+        const uint32_t to = stages + next_stage * S::STAGE;
 #pragma unroll
-        for (int y = 0; y < 2; y++)
+        for (int j = 0; j < S::ROWS / 8; j++)
+            load_lds(in ? A.w + (n0 + min(next_row + 8 * j + r, rows - 1)) * A.K + k : reinterpret_cast<const int8_t *>(kZeros),
+                     to + j * 1024);
 #pragma unroll
-            for (int x = 0; x < 2; x++)
-                acc[y][x] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lds[0][wm + 16 * y + i][g], lds[1][wn + 16 * x + i][g],
-                                                                  acc[y][x], 0, 0, 0);
-    }
+        for (int j = 0; j < EIGHTS; j++)
+            load_lds(in ? A.a + min(8 * j + r, (int)A.M - 1) * A.K + k : reinterpret_cast<const int8_t *>(kZeros),
+                     to + (S::ROWS / 8 + j) * 1024);
+        if (++next_step == steps) {
+            next_step = 0;
+            next_row += S::ROWS;
+        }
+        if (++next_stage == S::STAGES)
+            next_stage = 0;
+    };
+
+    __syncthreads();
 #pragma unroll
-    for (int x = 0; x < 2; x++) {
-        const int64_t n = n0 + wn + 16 * x + i;
-        if (n >= A.N)
-            continue;
-        const float sw = A.w_scales[n];
+    for (int i = 0; i < S::STAGES - 1; i++)
+        load();
+    const int row = lane & 15, g = lane >> 4;
+    const uint32_t first_w = row * 128 + (g ^ (lane & 7)) * 16;
+    const uint32_t first_a = S::ROWS * 128 + (EIGHTS == 1 ? row & 7 : row) * 128 + (g ^ (lane & 7)) * 16;
+    int stage = 0;
+    for (int tile = 0; tile < tiles; tile++) {
+        i32x4_t acc[2][S::TILES] = {};
+        for (int step = 0; step < steps; step++) {
+            wait<63, true>();  // what is overwritten has been read
+            load();
+            wait<(S::STAGES - 1) * S::LOADS, false>();
+            const char *const p = base + (wave * S::STAGES + stage) * S::STAGE;
 #pragma unroll
-        for (int y = 0; y < 2; y++)
+            for (int t = 0; t < 2; t++) {
+                i32x4_t fw[2], fa[S::TILES];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int64_t m = m0 + wm + 16 * y + 4 * g + e;
-                if (m < A.M)
-                    reinterpret_cast<typename Elem<T>::type *>(A.out)[m * A.out_stride + n] =
-                        (typename Elem<T>::type)((float)acc[y][x][e] * A.a_scales[m] * sw);
+                for (int i = 0; i < 2; i++)
+                    fw[i] = *reinterpret_cast<const i32x4_t *>(p + (first_w ^ 64 * t) + i * 2048);
+#pragma unroll
+                for (int i = 0; i < S::TILES; i++)
+                    fa[i] = *reinterpret_cast<const i32x4_t *>(p + (first_a ^ 64 * t) + i * 2048);
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int j = 0; j < S::TILES; j++)
+                        acc[i][j] = products(fw[i], fa[j], acc[i][j]);
             }
+            if (++stage == S::STAGES)
+                stage = 0;
+        }
+        // the waves' sums: [wave][token][row]; the tile after next has the same place, behind another barrier
+        int *const mine = sums + (tile & 1) * (S::SUMS / 4);
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < S::TILES; j++)
+                *reinterpret_cast<i32x4_t *>(mine + ((wave * S::TILES + j) * 16 + row) * S::ROW + 16 * i + 4 * g) = acc[i][j];
+        wait<63, true>();
+        barrier();
+#pragma unroll
+        for (int i = 0; i < S::TILES * 2; i++) {
+            const int m = i * 8 + (int)(threadIdx.x >> 5), n = (int)threadIdx.x & 31, at = tile * S::ROWS + n;
+            int sum = 0;
+#pragma unroll
+            for (int v = 0; v < S::WAVES; v++)
+                sum += mine[(v * S::TILES * 16 + m) * S::ROW + n];
+            if (m < A.M && at < rows)
+                reinterpret_cast<E *>(A.out)[m * A.out_stride + n0 + at] = (E)((float)sum * scales[S::MOST + m] * scales[at]);
+        }
+    }
+    wait<0, true>();
+}
+
+// ---- tiles ----------------------------------------------------------------------------------------
+
+// Which tile a workgroup has. Workgroups go to the eight XCDs in turn, each with its own second-level cache:
+// each XCD gets a run of tiles, in bands of kBand rows of tiles, down a band's column first, so that the tiles that
+// an XCD works on share their rows of either operand.
+constexpr int kBand = 4;
+__device__ __forceinline__ void tile_of(const GemmArgs &A, int block, int blocks, int &tm, int &tn)
+{
+    const int xcd = block & 7, each = blocks >> 3, more = blocks & 7;
+    const int at = xcd * each + min(xcd, more) + (block >> 3);
+    const int band = at / (kBand * A.tiles_n), in = at - band * kBand * A.tiles_n;
+    const int high = min(kBand, A.tiles_m - band * kBand);
+    const int column = in / high;  // a division runs on the vector unit
+    tn = __builtin_amdgcn_readfirstlane(column);
+    tm = __builtin_amdgcn_readfirstlane(band * kBand + in - column * high);
+}
+
+// SIZE x SIZE outputs a workgroup, a quarter each wave.
+template <int SIZE>
+struct Square {
+    static constexpr int STAGE = 2 * SIZE * 128, LOADS = STAGE / 4096, STAGES = 4;
+    static constexpr int BYTES = STAGES * STAGE, N = SIZE / 32;  // 16-row tiles of a wave, each way
+};
+
+template <int T, int SIZE>
+__global__ void __launch_bounds__(256) gemm_int8_tile_kernel(GemmArgs A)
+{
+    typedef Square<SIZE> S;
+    typedef typename Elem<T>::type E;
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    extern __shared__ i32x4_t lds[];  // [stage][a, w][row][piece]
+    __shared__ bool last;
+    char *const base = reinterpret_cast<char *>(lds);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = A.tiles_m * A.tiles_n, part = (int)blockIdx.x / tiles;
+    int tm, tn;
+    tile_of(A, (int)blockIdx.x - part * tiles, tiles, tm, tn);
+    const int64_t m0 = (int64_t)tm * SIZE, n0 = (int64_t)tn * SIZE;
+
+    const int r = threadIdx.x >> 3, piece = (lane & 7) ^ (r & 7);
+    const int8_t *const a0 = A.a + m0 * A.K, *const w0 = A.w + n0 * A.K;
+    const int last_a = (int)min(A.M - 1 - m0, (int64_t)SIZE - 1), last_w = (int)min(A.N - 1 - n0, (int64_t)SIZE - 1);
+    uint32_t src[2][SIZE / 32];
+#pragma unroll
+    for (int j = 0; j < SIZE / 32; j++) {
+        src[0][j] = (uint32_t)(min(r + 32 * j, last_a) * A.K + 16 * piece);
+        src[1][j] = (uint32_t)(min(r + 32 * j, last_w) * A.K + 16 * piece);
+    }
+    const uint32_t stages = (uint32_t)(uintptr_t)lds + wave * 1024;
+    const int first = part * A.each, end = min((A.K + 127) / 128, first + A.each);
+    const auto load = [&](int step, int stage) {
+        const int64_t k = step * 128;
+        const bool in = step < end && k + 16 * piece < A.K;
+#pragma unroll
+        for (int o = 0; o < 2; o++)
+#pragma unroll
+            for (int j = 0; j < SIZE / 32; j++)
+                load_lds(in ? (o ? w0 : a0) + k + src[o][j] : reinterpret_cast<const int8_t *>(kZeros),
+                         stages + stage * S::STAGE + o * SIZE * 128 + j * 4096);
+    };
+#pragma unroll
+    for (int i = 0; i < S::STAGES - 1; i++)
+        load(first + i, i);
+    const int row = lane & 15, g = lane >> 4, wm = (wave & 1) * (SIZE / 2), wn = (wave >> 1) * (SIZE / 2);
+    const uint32_t first_a = (wm + row) * 128 + (g ^ (lane & 7)) * 16, first_w = (SIZE + wn + row) * 128 + (g ^ (lane & 7)) * 16;
+    i32x4_t acc[S::N][S::N] = {};  // [16 of m][16 of n]
+    int stage = 0, next = S::STAGES - 1;
+    for (int step = first; step < end; step++) {
+        wait<(S::STAGES - 2) * S::LOADS, true>();  // this step has landed, the last one has been read
+        barrier();
+        load(step + S::STAGES - 1, next);
+        const char *const p = base + stage * S::STAGE;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            i32x4_t fa[S::N], fw[S::N];
+#pragma unroll
+            for (int i = 0; i < S::N; i++) {
+                fa[i] = *reinterpret_cast<const i32x4_t *>(p + (first_a ^ 64 * t) + i * 2048);
+                fw[i] = *reinterpret_cast<const i32x4_t *>(p + (first_w ^ 64 * t) + i * 2048);
+            }
+#pragma unroll
+            for (int i = 0; i < S::N; i++)
+#pragma unroll
+                for (int j = 0; j < S::N; j++)
+                    acc[i][j] = products(fw[j], fa[i], acc[i][j]);
+        }
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+        next = next + 1 == S::STAGES ? 0 : next + 1;
+    }
+    wait<0, true>();
+    if (A.splits > 1) {
+        const int tile = tm * A.tiles_n + tn;
+        constexpr int NUMBERS = S::N * S::N * 2;  // of 64 bits
+        unsigned long long *const parts = A.parts + (int64_t)tile * A.splits * NUMBERS * 256 + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < S::N; i++)
+#pragma unroll
+            for (int j = 0; j < S::N; j++)
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    put_shared(parts + ((int64_t)part * NUMBERS + (i * S::N + j) * 2 + e) * 256,
+                               (unsigned long long)(uint32_t)acc[i][j][2 * e + 1] << 32 | (uint32_t)acc[i][j][2 * e]);
+        wait<0, false>();  // every wave's, before the barrier
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = arrive_last(A.arrivals + (int64_t)tile * kLine, A.number, (unsigned)A.splits);
+        __syncthreads();
+        if (!last)
+            return;
+        for (int other = 0; other < A.splits; other++) {
+            if (other == part)
+                continue;
+#pragma unroll
+            for (int i = 0; i < S::N; i++)
+#pragma unroll
+                for (int j = 0; j < S::N; j++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const unsigned long long v = get_shared(parts + ((int64_t)other * NUMBERS + (i * S::N + j) * 2 + e) * 256);
+                        acc[i][j][2 * e] += (int)(uint32_t)v;
+                        acc[i][j][2 * e + 1] += (int)(v >> 32);
+                    }
+        }
+    }
+    float sw[S::N][4];
+#pragma unroll
+    for (int j = 0; j < S::N; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            sw[j][e] = A.w_scales[min(n0 + wn + 16 * j + 4 * g + e, A.N - 1)];
+#pragma unroll
+    for (int i = 0; i < S::N; i++) {
+        const int64_t m = m0 + wm + 16 * i + row;
+        if (m >= A.M)
+            continue;
+        const float sa = A.a_scales[m];
+#pragma unroll
+        for (int j = 0; j < S::N; j++) {
+            const int64_t n = n0 + wn + 16 * j + 4 * g;
+            E *const p = reinterpret_cast<E *>(A.out) + m * A.out_stride + n;
+            E4 v;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[e] = (E)((float)acc[i][j][e] * sa * sw[j][e]);
+            if (A.vec && n + 4 <= A.N) {
+                *reinterpret_cast<E4 *>(p) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (n + e < A.N)
+                        p[e] = v[e];
+            }
+        }
     }
 }
 
+// ---- 256 x 256 ------------------------------------------------------------------------------------
+
+constexpr int kUnit = 128 * 128;  // bytes of a half of either operand's rows, a line each
+constexpr int kLargeBytes = 8 * kUnit;
+
+// Eight waves of 128 x 64 outputs each, two waves a SIMD, which alternate: while one multiplies, the other reads its
+// operands and starts loads, a barrier between. A line of K is four such turns, one for each pair of halves of
+// the wave's rows: (A0, B0), (A0, B1), (A1, B1), (A1, B0). What a turn reads can be loaded over two turns
+// later, when both waves have read it, and so each unit is loaded a step and a half before it is read.
+template <int T>
+__global__ void __launch_bounds__(512, 2) gemm_int8_large_kernel(GemmArgs A)
+{
+    extern __shared__ i32x4_t lds[];  // [step & 1][A0, A1, B0, B1][128 rows][8 pieces]
+    typedef typename Elem<T>::type E;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = wave & 1, wc = wave >> 1;  // waves w and w + 4 share a SIMD
+    int tm, tn;
+    tile_of(A, (int)blockIdx.x, A.tiles_m * A.tiles_n, tm, tn);
+    const int64_t m0 = (int64_t)tm * 256, n0 = (int64_t)tn * 256;
+
+    // loading: a thread has a piece of rows t / 8 and t / 8 + 64 of each unit
+    const int piece = (threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7);
+    const int8_t *const a0 = A.a + m0 * A.K, *const w0 = A.w + n0 * A.K;
+    const int last_a = (int)min(A.M - 1 - m0, (int64_t)255), last_w = (int)min(A.N - 1 - n0, (int64_t)255);
+    uint32_t src[4][2];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const int r = (int)(threadIdx.x >> 3) + 64 * j;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            src[h][j] = (uint32_t)(min((r >> 6) * 128 + h * 64 + (r & 63), last_a) * A.K + 16 * piece);
+            src[2 + h][j] = (uint32_t)(min((r >> 5) * 64 + h * 32 + (r & 31), last_w) * A.K + 16 * piece);
+        }
+    }
+    const uint32_t lds_base = (uint32_t)(uintptr_t)lds + wave * 1024;
+    const auto load = [&](int step, int unit) {
+        const int k = step * 128;
+        const bool in = k + 16 * piece < A.K;
+        const int8_t *const base = (unit < 2 ? a0 : w0) + k;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            load_lds(in ? base + src[unit][j] : reinterpret_cast<const int8_t *>(kZeros),
+                     lds_base + ((step & 1) * 4 + unit) * kUnit + j * 8192);
+    };
+
+    i32x4_t fa[4][2], fb[2][2][2];
+    const int row = lane & 15, g = lane >> 4;
+    // a lane's first piece of its row; the other is four pieces on, before the exchange of pieces
+    const uint32_t first_a = (wr * 64 + row) * 128 + (g ^ (lane & 7)) * 16, first_b = (wc * 32 + row) * 128 + (g ^ (lane & 7)) * 16;
+    const auto piece_at = [&](uint32_t first, int buffer, int t, int at) {
+        return *reinterpret_cast<const i32x4_t *>(reinterpret_cast<const char *>(lds) + ((first ^ 64 * t) + buffer * 4 * kUnit) + at);
+    };
+    const auto read_a = [&](int buffer, int h) {
+        const uint32_t first = here(first_a);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                fa[i][t] = piece_at(first, buffer, t, h * kUnit + i * 2048);
+    };
+    const auto read_b = [&](int buffer, int h, int to) {
+        const uint32_t first = here(first_b);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                fb[to][j][t] = piece_at(first, buffer, t, (2 + h) * kUnit + j * 2048);
+    };
+    i32x4_t acc[2][4][2][2] = {};  // [half of A][i][half of B][j]
+    const auto multiply = [&](int ha, int hb, int from) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    acc[ha][i][hb][j] = products(fb[from][j][t], fa[i][t], acc[ha][i][hb][j]);
+        __builtin_amdgcn_s_setprio(0);
+        barrier();
+    };
+    // the end of a turn's reads: they are in registers, and what the next turn reads has landed (of the eight units
+    // under way, the six last may be on their way)
+    const auto landed = [&]() {
+        wait<12, true>();
+        barrier();
+    };
+
+    // units in the order in which they are read
+#pragma unroll
+    for (int step = 0; step < 2; step++) {
+        load(step, 2);
+        load(step, 0);
+        load(step, 3);
+        load(step, 1);
+    }
+    wait<12, false>();
+    barrier();
+    read_b(0, 0, 0);
+    wait<63, true>();
+    barrier();
+    if (wave >= 4)  // the second wave of each SIMD is half a turn behind
+        barrier();
+    const int steps = (A.K + 127) / 128;
+    const auto one = [&](int step, int buffer) {
+        read_a(buffer, 0);
+        load(step + 2, 2);
+        landed();
+        multiply(0, 0, buffer);
+        read_b(buffer, 1, buffer ^ 1);
+        load(step + 2, 0);
+        landed();
+        multiply(0, 1, buffer ^ 1);
+        read_a(buffer, 1);
+        load(step + 2, 3);
+        landed();
+        multiply(1, 1, buffer ^ 1);
+        read_b(buffer ^ 1, 0, buffer ^ 1);  // the next step's
+        load(step + 2, 1);
+        landed();
+        multiply(1, 0, buffer);
+    };
+    for (int step = 0; step < steps; step += 2) {
+        one(step, 0);
+        if (step + 1 < steps)
+            one(step + 1, 1);
+    }
+    if (wave < 4)
+        barrier();
+    wait<0, true>();
+    barrier();
+
+    // A lane has token row of 16 and four rows of w, 4g .. 4g + 3: sixteen tokens at a time go through the wave's own
+    // part of LDS to be written as whole lines.
+    constexpr int VEC = 16 / sizeof(E), LANES = 64 / VEC, STRIDE = 64 + VEC;  // lanes and elements a token's row of 64
+    typedef E EV __attribute__((ext_vector_type(VEC)));
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    E *const stage = reinterpret_cast<E *>(lds) + wave * 16 * STRIDE;
+    const int64_t n_wave = n0 + wc * 64, m_wave = m0 + wr * 128;
+    float sw[2][2][4];
+#pragma unroll
+    for (int hb = 0; hb < 2; hb++)
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                sw[hb][j][e] = A.w_scales[min(n_wave + hb * 32 + j * 16 + 4 * g + e, A.N - 1)];
+#pragma unroll
+    for (int ha = 0; ha < 2; ha++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int64_t m = m_wave + ha * 64 + i * 16;
+            if (m >= A.M)
+                continue;
+            const float sa = A.a_scales[min(m + row, A.M - 1)];
+#pragma unroll
+            for (int hb = 0; hb < 2; hb++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    E4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        v[e] = (E)((float)acc[ha][i][hb][j][e] * sa * sw[hb][j][e]);
+                    *reinterpret_cast<E4 *>(stage + row * STRIDE + hb * 32 + j * 16 + 4 * g) = v;
+                }
+#pragma unroll
+            for (int q = 0; q < 16 * LANES / 64; q++) {
+                const int at = q * (64 / LANES) + lane / LANES, c = lane % LANES * VEC;
+                const EV v = *reinterpret_cast<const EV *>(stage + at * STRIDE + c);
+                E *const p = reinterpret_cast<E *>(A.out) + (m + at) * A.out_stride + n_wave + c;
+                if (m + at >= A.M)
+                    continue;
+                if (A.vec && n_wave + c + VEC <= A.N) {
+                    *reinterpret_cast<EV *>(p) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; e++)
+                        if (n_wave + c + e < A.N)
+                            p[e] = v[e];
+                }
+            }
+        }
+}
+
+// ---- host -----------------------------------------------------------------------------------------
+
 static bool gemm_fit(int64_t M, int64_t N, int64_t K)
 {
-    return M >= 0 && N >= 0 && M <= 65535 * 64 && N <= INT32_MAX && K >= 16 && K % 16 == 0 && K <= PN_GEMM_INT8_MAX_K;
+    return M >= 0 && N >= 0 && M <= INT32_MAX && N <= INT32_MAX && K >= 16 && K % 16 == 0 && K <= PN_GEMM_INT8_MAX_K &&
+           ((M + 63) / 64) * ((N + 63) / 64) <= INT32_MAX / 64;
+}
+
+// How a product is cut.
+struct GemmCut {
+    int size;    // of a tile: 0 for the stream
+    int splits;  // parts of K
+    int each;    // lines of 128 of a part
+    int64_t workspace;
+};
+static GemmCut gemm_cut(int64_t M, int64_t N, int64_t K)
+{
+    const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const auto tiles = [&](int size) { return up(M, size) * up(N, size); };
+    const int64_t cus = device_cus(), lines = up(K, 128);
+    GemmCut c = {};
+    c.splits = 1;
+    c.each = (int)lines;
+    if (M <= 32)
+        return c;
+    c.size = tiles(256) >= cus * 3 / 4 ? 256 : tiles(128) >= cus ? 128 : 64;
+    if (c.size == 64) {
+        const int64_t t = tiles(64);
+        // two workgroups a CU, each with at least eight lines
+        c.splits = (int)std::max<int64_t>(1, std::min(2 * cus / t, lines / 8));
+        c.each = (int)up(lines, c.splits);
+        c.splits = (int)up(lines, c.each);
+        if (c.splits > 1)
+            c.workspace = t * kLine * 8 + t * c.splits * 64 * 64 * 4;
+    }
+    return c;
+}
+
+// Launches kernel KERN with its dynamic LDS.
+template <auto KERN>
+static int launch_gemm(const GemmArgs &A, unsigned blocks, int threads, int bytes, hipStream_t s)
+{
+    if (!lds_limit_once<KERN>(bytes))
+        return PN_ERR_HIP;
+    hipLaunchKernelGGL(KERN, dim3(blocks), dim3(threads), bytes, s, A);
+    return launch_status();
+}
+
+template <int T>
+static int run_gemm(GemmArgs A, const GemmCut &c, hipStream_t s)
+{
+    if (c.size == 0) {
+        // one workgroup a CU, as many rows each as it takes
+        const int64_t cus = device_cus();
+        const unsigned blocks = (unsigned)std::max(std::min((A.N + 7) / 8, cus), (A.N + 1023) / 1024);
+        return A.M <= 8    ? launch_gemm<gemm_int8_stream_kernel<T, 1>>(A, blocks, 256, Stream<1>::BYTES, s)
+               : A.M <= 16 ? launch_gemm<gemm_int8_stream_kernel<T, 2>>(A, blocks, 256, Stream<2>::BYTES, s)
+                           : launch_gemm<gemm_int8_stream_kernel<T, 4>>(A, blocks, 256, Stream<4>::BYTES, s);
+    }
+    A.tiles_m = (int)((A.M + c.size - 1) / c.size);
+    A.tiles_n = (int)((A.N + c.size - 1) / c.size);
+    A.splits = c.splits;
+    A.each = c.each;
+    const unsigned blocks = (unsigned)A.tiles_m * A.tiles_n * c.splits;
+    return c.size == 256   ? launch_gemm<gemm_int8_large_kernel<T>>(A, blocks, 512, kLargeBytes, s)
+           : c.size == 128 ? launch_gemm<gemm_int8_tile_kernel<T, 128>>(A, blocks, 256, Square<128>::BYTES, s)
+                           : launch_gemm<gemm_int8_tile_kernel<T, 64>>(A, blocks, 256, Square<64>::BYTES, s);
 }
 
 }  // namespace pn
@@ -74,7 +609,7 @@ using namespace pn;
 
 extern "C" int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
-    return 0;
+    return gemm_fit(M, N, K) && M > 0 && N > 0 ? gemm_cut(M, N, K).workspace : 0;
 }
 
 extern "C" int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t *w,
@@ -92,17 +627,36 @@ extern "C" int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, c
         return PN_ERR_NULL;
     if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(out, size))
         return PN_ERR_ALIGN;
+    const GemmCut c = gemm_cut(M, N, K);
+    if (c.workspace > 0) {
+        if (!workspace)
+            return PN_ERR_NULL;
+        if (!aligned(workspace, 16))
+            return PN_ERR_ALIGN;
+        if (workspace_bytes < c.workspace)
+            return PN_ERR_WORKSPACE;
+    }
     const int st = check_device();
     if (st != PN_OK)
         return st;
-    const GemmArgs A{a, w, a_scales, w_scales, M, N, out_stride, (int)K, out};
-    const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
+    GemmArgs A = {};
+    A.a = a;
+    A.w = w;
+    A.a_scales = a_scales;
+    A.w_scales = w_scales;
+    A.M = M;
+    A.N = N;
+    A.out_stride = out_stride;
+    A.K = (int)K;
+    A.out = out;
+    A.vec = aligned(out, 16) && (out_stride * size & 15) == 0;
+    if (c.workspace > 0) {
+        A.number = call_number();
+        A.arrivals = (unsigned long long *)workspace;
+        A.parts = A.arrivals + ((M + 63) / 64) * ((N + 63) / 64) * kLine;
+    }
     hipStream_t s = (hipStream_t)stream;
-    if (type == PN_F32)
-        hipLaunchKernelGGL((gemm_int8_kernel<PN_F32>), grid, dim3(256), 0, s, A);
-    else if (type == PN_BF16)
-        hipLaunchKernelGGL((gemm_int8_kernel<PN_BF16>), grid, dim3(256), 0, s, A);
-    else
-        hipLaunchKernelGGL((gemm_int8_kernel<PN_F16>), grid, dim3(256), 0, s, A);
-    return launch_status();
+    return type == PN_F32    ? run_gemm<PN_F32>(A, c, s)
+           : type == PN_BF16 ? run_gemm<PN_BF16>(A, c, s)
+                             : run_gemm<PN_F16>(A, c, s);
 }
