@@ -12,18 +12,19 @@
 // after the first batches is rare (about top / n of the logits at the n-th); then each lane offers its
 // best, and few are put in one by one, many are sorted among the lanes and merged.
 //
-// Memory bound for long rows. A wave reads batches of 4 KB; a row is shared by up to 64 workgroups where
-// there are few, the last to arrive joins them (pn_arrive.h).
+// Memory bound for long rows: 2047 of 248,320 bf16 204 us with the five likeliest (5.0 TB/s; a copy reaches 4.9, the
+// exponentials and the rest would take about 150 by themselves). One row of fp32 15.6 us with 20, 10.1 with none, of
+// which a launch and a first load are 5. A wave reads batches of 4 KB, one ahead; a row is shared by up to 64
+// workgroups where there are few, and the last to arrive joins them (pn_arrive.h).
 #include <float.h>
 
 #include <algorithm>
 
 #include "pn_arrive.h"
 #include "pn_cache.h"
+#include "pn_lanes.h"
 
 namespace pn {
-
-typedef unsigned long long u64;
 
 struct LogArgs {
     const void *logits;
@@ -48,6 +49,20 @@ struct Sums {
 
 __device__ __forceinline__ float greater(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
 
+// The largest and the smallest of three, NaN aside. (Left to itself the compiler quiets each operand first.)
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float r;
+    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // l and t relative to `from` as they are relative to `to`.
 __device__ __forceinline__ void rescale(float &l, float &t, float from, float to, float exp2_scale)
 {
@@ -67,10 +82,16 @@ __device__ __forceinline__ Sums join(Sums a, Sums b, float exp2_scale)
     return Sums{m, a.l + b.l, a.t + b.t, a.count + b.count};
 }
 
-__device__ __forceinline__ Sums other_lane(Sums a, int mask)
+// The sums of all lanes, in every lane.
+template <int MASK = 1>
+__device__ __forceinline__ Sums over_lanes(Sums a, float exp2_scale)
 {
-    return Sums{__shfl_xor(a.m, mask, 64), __shfl_xor(a.l, mask, 64), __shfl_xor(a.t, mask, 64),
-                __shfl_xor(a.count, mask, 64)};
+    const auto other = [](auto v) { return __builtin_bit_cast(decltype(v), moved_by<MASK>(__builtin_bit_cast(uint32_t, v))); };
+    a = join(a, Sums{other(a.m), other(a.l), other(a.t), other(a.count)}, exp2_scale);
+    if constexpr (MASK < 32)
+        return over_lanes<2 * MASK>(a, exp2_scale);
+    else
+        return a;
 }
 
 // A logit and its token as a key: larger logits first, then lower numbers; never 0.
@@ -92,31 +113,58 @@ __device__ __forceinline__ u64 lane_key(u64 v, int lane)
            (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// One step of a bitonic network over the lanes.
-__device__ __forceinline__ u64 exchange(u64 v, int stride, bool larger)
+// The keys of this lane and of the one STRIDE away, the lower lane's first, in both lanes.
+template <int STRIDE>
+__device__ __forceinline__ void pair_of(u64 v, u64 &low, u64 &high)
 {
-    const u64 o = __shfl_xor(v, stride, 64);
-    return (o > v) == larger ? o : v;
+    uint32_t l[2], h[2];
+    const uint32_t w[2] = {(uint32_t)v, (uint32_t)(v >> 32)};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        if constexpr (STRIDE == 32) {
+            const auto p = __builtin_amdgcn_permlane32_swap(w[i], w[i], false, false);
+            l[i] = p[0];
+            h[i] = p[1];
+        } else {
+            const auto p = __builtin_amdgcn_permlane16_swap(w[i], w[i], false, false);
+            l[i] = p[0];
+            h[i] = p[1];
+        }
+    }
+    low = (u64)l[1] << 32 | l[0];
+    high = (u64)h[1] << 32 | h[0];
+}
+// One step of a bitonic network over the lanes: the larger or the smaller of the two that are STRIDE apart.
+template <int STRIDE>
+__device__ __forceinline__ u64 exchange(u64 v, bool larger)
+{
+    if constexpr (STRIDE >= 16) {
+        u64 a, b;
+        pair_of<STRIDE>(v, a, b);
+        return (a > b) == larger ? a : b;
+    } else {
+        const u64 o = moved_by<STRIDE>(v);
+        return (o > v) == larger ? o : v;
+    }
+}
+template <int SIZE, int STRIDE>
+__device__ __forceinline__ u64 network(u64 v, int lane)
+{
+    v = exchange<STRIDE>(v, ((lane & STRIDE) == 0) == ((lane & SIZE) == 0));
+    if constexpr (STRIDE > 1)
+        return network<SIZE, STRIDE / 2>(v, lane);
+    else if constexpr (SIZE < 64)
+        return network<SIZE * 2, SIZE>(v, lane);
+    else
+        return v;
 }
 // The lanes' keys in falling order.
-__device__ __forceinline__ u64 sorted(u64 v, int lane)
-{
-#pragma unroll
-    for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-        for (int stride = size / 2; stride > 0; stride /= 2)
-            v = exchange(v, stride, ((lane & stride) == 0) == ((lane & size) == 0));
-    return v;
-}
+__device__ __forceinline__ u64 sorted(u64 v, int lane) { return network<2, 1>(v, lane); }
 // The 64 largest of two lists in falling order.
 __device__ __forceinline__ u64 merged(u64 a, u64 b, int lane)
 {
-    const u64 r = __shfl(b, 63 - lane, 64);
-    u64 v = a > r ? a : r;
-#pragma unroll
-    for (int stride = 32; stride > 0; stride /= 2)
-        v = exchange(v, stride, (lane & stride) == 0);
-    return v;
+    const u64 r = moved_by<63>(b);
+    return network<64, 32>(a > r ? a : r, lane);
 }
 // `key` put into the list (its last one falls out).
 __device__ __forceinline__ u64 inserted(u64 list, u64 key, int lane)
@@ -152,36 +200,49 @@ struct Batch {
     }
 };
 
-// Puts what passes `thr` of a batch whose first logit of this lane is token `first` into the list.
+// Puts what passes `thr` of a batch whose first logit of this lane is token `first` into the list; m is the lane's
+// largest.
 template <int T>
-__device__ __forceinline__ void take(const float (&x)[Batch<T>::PER], int first, int top, int lane, u64 &list, float &thr)
+__device__ __forceinline__ void take(const float (&x)[Batch<T>::PER], float m, int first, int top, int lane, u64 &list,
+                                     float &thr)
 {
     constexpr int VEC = Batch<T>::VEC, PER = Batch<T>::PER;
-    uint32_t left = 0;
+    const auto token = [&](int j) { return first + j / VEC * 64 * VEC + j % VEC; };
+    if (__popcll(__ballot(m > thr)) <= 4) {
+        // few lanes: each logit that passes is put in by itself
 #pragma unroll
-    for (int j = 0; j < PER; j++)
-        left |= x[j] > thr ? 1u << j : 0u;
-    while (__any(left != 0)) {
-        float best = -INFINITY;
-        int at = 0;
+        for (int j = 0; j < PER; j++) {
+            u64 offers = __ballot(x[j] > thr);
+            if (offers) {
+                const u64 key = key_of(x[j], token(j));
+                for (; offers; offers &= offers - 1)
+                    list = inserted(list, lane_key(key, __ffsll(offers) - 1), lane);
+            }
+        }
+    } else {
+        // each lane offers its best, and those that pass are sorted among the lanes and merged, until none passes
+        uint32_t left = 0;
 #pragma unroll
         for (int j = 0; j < PER; j++)
-            if ((left >> j & 1) && x[j] > best) {
-                best = x[j];
-                at = j;
-            }
-        u64 key = key_of(best, first + at / VEC * 64 * VEC + at % VEC);
-        const bool in = left != 0 && key > lane_key(list, top - 1);
-        left = in ? left & ~(1u << at) : 0;
-        u64 offers = __ballot(in);
-        if (__popcll(offers) <= 8) {
-            while (offers) {
-                const int from = __ffsll(offers) - 1;
-                offers &= offers - 1;
-                list = inserted(list, lane_key(key, from), lane);
-            }
-        } else {
-            list = merged(list, sorted(in ? key : 0, lane), lane);
+            left |= x[j] > thr ? 1u << j : 0u;
+        while (__any(left != 0)) {
+            float best = -INFINITY;
+            int at = 0;
+#pragma unroll
+            for (int j = 0; j < PER; j++)
+                if ((left >> j & 1) && x[j] > best) {
+                    best = x[j];
+                    at = j;
+                }
+            const u64 key = key_of(best, token(at));
+            const bool in = left != 0 && key > lane_key(list, top - 1);
+            left = in ? left & ~(1u << at) : 0;
+            u64 offers = __ballot(in);
+            if (__popcll(offers) > 8)
+                list = merged(list, sorted(in ? key : 0, lane), lane);
+            else
+                for (; offers; offers &= offers - 1)
+                    list = inserted(list, lane_key(key, __ffsll(offers) - 1), lane);
         }
     }
     const u64 last = lane_key(list, top - 1);
@@ -212,18 +273,38 @@ __device__ __forceinline__ void write_row(const LogArgs &A, int64_t row, Sums a,
     }
 }
 
-template <int T>
-__global__ void __launch_bounds__(256) logprobs_kernel(LogArgs A)
+// The lists of a workgroup's waves into the first one's, by twos.
+template <int WAVES>
+__device__ __forceinline__ u64 over_waves(u64 list, u64 (&lds)[WAVES][64], int wave, int lane)
+{
+#pragma unroll
+    for (int n = WAVES / 2; n > 0; n /= 2) {
+        if (wave >= n && wave < 2 * n)
+            lds[wave][lane] = list;
+        __syncthreads();
+        if (wave < n)
+            list = merged(list, lds[wave + n][lane], lane);
+    }
+    return list;
+}
+
+template <int T, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
 {
     typedef Batch<T> B;
     typedef typename B::E E;
-    __shared__ Sums lds_sums[4];
-    __shared__ u64 lds_list[4][64];
+    __shared__ Sums lds_sums[WAVES];
+    __shared__ u64 lds_list[2][WAVES][64];
     __shared__ bool last;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = blockIdx.x / (unsigned)A.groups;
     const int group = (int)(blockIdx.x - row * A.groups);
     const E *const x_row = reinterpret_cast<const E *>(A.logits) + row * A.stride;
+
+    int batch = group * WAVES + wave;
+    B next;
+    if (batch < A.batches)
+        next.load(x_row, batch * B::ALL, A.V, lane);
     const int token = A.tokens ? A.tokens[row] : -1;
     const bool has_token = token >= 0 && token < A.V;
     const float token_logit = has_token ? (float)x_row[token] : INFINITY;
@@ -232,59 +313,61 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogArgs A)
     float ref = 0.0f;  // what l and t are relative to: m, or anything while they are zero
     u64 list = 0;
     float thr = A.top > 0 ? -INFINITY : INFINITY;
-    int batch = group * 4 + wave;
-    B next;
-    if (batch < A.batches)
-        next.load(x_row, batch * B::ALL, A.V, lane);
     while (batch < A.batches) {
         const int first = batch * B::ALL + lane * B::VEC;
         const B now = next;
-        batch += A.groups * 4;
+        batch += A.groups * WAVES;
         if (batch < A.batches)
             next.load(x_row, batch * B::ALL, A.V, lane);
         float x[B::PER];
 #pragma unroll
         for (int j = 0; j < B::PER; j++)
             x[j] = (float)now.v[j / B::VEC][j % B::VEC];
-        float m = x[0];
+        float m = -INFINITY, low = INFINITY;
 #pragma unroll
-        for (int j = 1; j < B::PER; j++)
-            m = greater(m, x[j]);
+        for (int j = 0; j < B::PER; j += 2) {
+            m = max3(m, x[j], x[j + 1]);
+            low = min3(low, x[j], x[j + 1]);
+        }
         if (__any(m > thr))
-            take<T>(x, first, A.top, lane, list, thr);
+            take<T>(x, m, first, A.top, lane, list, thr);
+        if (__any(m > token_logit))
+#pragma unroll
+            for (int j = 0; j < B::PER; j++)
+                a.count += x[j] > token_logit;
         m = greater(a.m, m);
         if (m > a.m) {
             rescale(a.l, a.t, ref, m, A.exp2_scale);
             a.m = ref = m;
         }
+        // e is 0 where d is -infinity, and the product with it must be too
+        const auto add = [&](auto masked) {
 #pragma unroll
-        for (int j = 0; j < B::PER; j++) {
-            const float d = x[j] - ref, e = __builtin_amdgcn_exp2f(d * A.exp2_scale);
-            a.l += e;
-            a.t = __builtin_fmaf(e, greater(d, -FLT_MAX), a.t);  // nothing where e is 0 and d -infinity
-            a.count += x[j] > token_logit;
-        }
+            for (int j = 0; j < B::PER; j++) {
+                const float d = x[j] - ref, e = __builtin_amdgcn_exp2f(d * A.exp2_scale);
+                a.l += e;
+                a.t = __builtin_fmaf(e, masked.value ? greater(d, -FLT_MAX) : d, a.t);
+            }
+        };
+        if (__any(low - ref == -INFINITY))
+            add(std::true_type());
+        else
+            add(std::false_type());
     }
-#pragma unroll
-    for (int mask = 1; mask < 64; mask *= 2)
-        a = join(a, other_lane(a, mask), A.exp2_scale);
+    a = over_lanes(a, A.exp2_scale);
 
     // the workgroup's waves into the first
     if (lane == 0)
         lds_sums[wave] = a;
-    lds_list[wave][lane] = list;
-    __syncthreads();
+    list = over_waves<WAVES>(list, lds_list[0], wave, lane);  // (with a barrier)
     if (wave == 0) {
-        a = join(join(lds_sums[0], lds_sums[1], A.exp2_scale), join(lds_sums[2], lds_sums[3], A.exp2_scale), A.exp2_scale);
-        if (A.top > 0)
-            for (int w = 1; w < 4; w++)
-                list = merged(list, lds_list[w][lane], lane);
-    }
-    if (A.groups == 1) {
-        if (wave == 0)
+        a = lane < WAVES ? lds_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f, 0};
+        a = over_lanes(a, A.exp2_scale);
+        if (A.groups == 1)
             write_row(A, row, a, list, lane, token_logit, has_token);
-        return;
     }
+    if (A.groups == 1)
+        return;
     if (wave == 0) {
         const int64_t at = row * A.groups + group;
         if (lane == 0) {
@@ -300,30 +383,30 @@ __global__ void __launch_bounds__(256) logprobs_kernel(LogArgs A)
     __syncthreads();
     if (!last)
         return;
-    // the groups' lists dealt to the waves
-    if (A.top > 0) {
-        list = 0;
-        for (int g = wave; g < A.groups; g += 4)
-            list = merged(list, lane < A.top ? get_shared(A.keys + (row * A.groups + g) * A.top + lane) : 0, lane);
-        lds_list[wave][lane] = list;
+    // the groups' lists dealt to the waves, read at once, merged by twos
+    constexpr int EACH = 64 / WAVES;
+    u64 in[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; i++) {
+        const int g = wave + WAVES * i;
+        in[i] = g < A.groups && lane < A.top ? get_shared(A.keys + (row * A.groups + g) * A.top + lane) : 0;
     }
-    __syncthreads();
-    if (wave != 0)
-        return;
     a = Sums{-INFINITY, 0.0f, 0.0f, 0};
-    if (lane < A.groups) {
+    if (wave == 0 && lane < A.groups) {
         const u64 *const p = A.parts + 2 * (row * A.groups + lane);
         const u64 u = get_shared(p), v = get_shared(p + 1);
         a = Sums{__builtin_bit_cast(float, (uint32_t)u), __builtin_bit_cast(float, (uint32_t)(u >> 32)),
                  __builtin_bit_cast(float, (uint32_t)v), (int)(v >> 32)};
     }
 #pragma unroll
-    for (int mask = 1; mask < 64; mask *= 2)
-        a = join(a, other_lane(a, mask), A.exp2_scale);
-    if (A.top > 0)
-        for (int w = 1; w < 4; w++)
-            list = merged(list, lds_list[w][lane], lane);
-    write_row(A, row, a, list, lane, token_logit, has_token);
+    for (int n = EACH / 2; n > 0; n /= 2)
+        if (A.groups > WAVES * n)
+#pragma unroll
+            for (int i = 0; i < n; i++)
+                in[i] = merged(in[i], in[i + n], lane);
+    list = over_waves<WAVES>(in[0], lds_list[1], wave, lane);
+    if (wave == 0)
+        write_row(A, row, over_lanes(a, A.exp2_scale), list, lane, token_logit, has_token);
 }
 
 // A batch has 1024 logits of four bytes or 2048 of two.
@@ -333,10 +416,27 @@ static int log_batches(int type, int64_t V)
     return (int)((V + all - 1) / all);
 }
 
-// Workgroups of a row: enough in all to fill the memory pipe, a batch at least for each wave.
+// Waves of a workgroup and workgroups of a row. Few rows: large workgroups, as many as fill the machine, since
+// arrivals at a row's word come one after another and a wave's list is joined sooner in LDS (one row: 15.6 us, 17.8 by
+// 61 workgroups of four waves). Many rows: small ones, half the machine at least; each share of a row begins its list
+// anew, which costs about as long as 30,000 of its logits (1023 rows of 248,320 fp32, top 64: 199 us whole, 217 in two).
+static int log_waves(int64_t R) { return R < 256 ? 16 : 4; }
 static int log_groups(int64_t R, int batches)
 {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (batches + 3) / 4), (1024 + R - 1) / R));
+    const int waves = log_waves(R);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (batches + waves - 1) / waves),
+                                                       ((waves == 16 ? 256 : 512) + R - 1) / R));
+}
+
+template <int T>
+static int launch_log(const LogArgs &A, int64_t R, hipStream_t s)
+{
+    const dim3 grid((unsigned)(R * A.groups));
+    if (log_waves(R) == 16)
+        hipLaunchKernelGGL((logprobs_kernel<T, 16>), grid, dim3(1024), 0, s, A);
+    else
+        hipLaunchKernelGGL((logprobs_kernel<T, 4>), grid, dim3(256), 0, s, A);
+    return launch_status();
 }
 
 static bool logits_fit(int64_t R, int64_t V, int top)
@@ -352,9 +452,8 @@ extern "C" int64_t pn_logprobs_workspace_bytes(int64_t R, int64_t V, int top)
 {
     if (!logits_fit(R, V, top) || R == 0)
         return 0;
-    // of the type that has more batches
-    const int groups = log_groups(R, log_batches(PN_F32, V));
-    return groups == 1 ? 0 : R * kLine * 8 + R * groups * (2 + top) * 8;
+    // of the type that has more batches, and the same whether a row is shared or not
+    return R * kLine * 8 + R * log_groups(R, log_batches(PN_F32, V)) * (2 + top) * 8;
 }
 
 extern "C" int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t workspace_bytes, void *stream)
@@ -368,20 +467,15 @@ extern "C" int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t w
         return PN_ERR_SHAPE;
     if (a->R == 0)
         return PN_OK;
-    if (!a->logits || ((a->logprob || a->rank) && !a->tokens) || (a->top > 0 && (!a->top_ids || !a->top_logprobs)))
+    if (!a->logits || !workspace || ((a->logprob || a->rank) && !a->tokens) || (a->top > 0 && (!a->top_ids || !a->top_logprobs)))
         return PN_ERR_NULL;
     if (!aligned(a->logits, size) || !aligned(a->tokens, 4) || !aligned(a->logprob, 4) || !aligned(a->rank, 4) ||
         !aligned(a->entropy, 4) || !aligned(a->lse, 4) || !aligned(a->top_ids, 4) || !aligned(a->top_logprobs, 4))
         return PN_ERR_ALIGN;
-    const int64_t need = pn_logprobs_workspace_bytes(a->R, a->V, a->top);
-    if (need > 0) {
-        if (!workspace)
-            return PN_ERR_NULL;
-        if (!aligned(workspace, 16))
-            return PN_ERR_ALIGN;
-        if (workspace_bytes < need)
-            return PN_ERR_WORKSPACE;
-    }
+    if (!aligned(workspace, 16))
+        return PN_ERR_ALIGN;
+    if (workspace_bytes < pn_logprobs_workspace_bytes(a->R, a->V, a->top))
+        return PN_ERR_WORKSPACE;
     const int st = check_device();
     if (st != PN_OK)
         return st;
@@ -405,13 +499,8 @@ extern "C" int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t w
     A.arrivals = (u64 *)workspace;
     A.parts = A.arrivals + a->R * kLine;
     A.keys = A.parts + a->R * A.groups * 2;
-    const dim3 grid((unsigned)(a->R * A.groups));
     hipStream_t s = (hipStream_t)stream;
-    if (a->type == PN_F32)
-        hipLaunchKernelGGL((logprobs_kernel<PN_F32>), grid, dim3(256), 0, s, A);
-    else if (a->type == PN_BF16)
-        hipLaunchKernelGGL((logprobs_kernel<PN_BF16>), grid, dim3(256), 0, s, A);
-    else
-        hipLaunchKernelGGL((logprobs_kernel<PN_F16>), grid, dim3(256), 0, s, A);
-    return launch_status();
+    return a->type == PN_F32    ? launch_log<PN_F32>(A, a->R, s)
+           : a->type == PN_BF16 ? launch_log<PN_BF16>(A, a->R, s)
+                                : launch_log<PN_F16>(A, a->R, s);
 }
