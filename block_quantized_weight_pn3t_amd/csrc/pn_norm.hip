@@ -8,11 +8,14 @@
 // and written once. One workgroup a row, or one wave where the row fits it: no barrier, four rows a
 // workgroup.
 //
-// Products h w are exact in 64 bits. A code is computed in fp32, where it is off by less than 1e-4, and in
-// 64 bits, by the definition, where it lies that near to a border (two numbers in ten thousand).
+// Codes are those of the definition in 64 bits, computed in 32: 127 / T and its product are off by less than 5e-5
+// there, and only where a quotient lies that near to a border between two codes (one number in ten thousand) is it
+// worked out in 64 bits. T has to be exact for that: a product of two 16-bit numbers is in fp32, one with an fp32
+// number is taken in 64 bits. Squares are summed in 64 bits.
 #include <float.h>
 
 #include "pn_cache.h"
+#include "pn_lanes.h"
 
 namespace pn {
 
@@ -28,74 +31,110 @@ struct NormArgs {
 };
 
 
-// N elements at p[at], one load of 16 bytes for each eight (two for fp32).
-template <int T, int N>
-__device__ __forceinline__ void load_n(const void *p, int64_t at, float (&x)[N])
+constexpr int VEC = 8;  // elements a thread loads at a time
+
+// The elements from p[at] on that a row of K has, zeros past its end. Rows may begin anywhere: the type says that a
+// load of 16 bytes is aligned to an element only, which the memory takes.
+template <int T, bool WHOLE>
+__device__ __forceinline__ void load_n(const void *p, int64_t row, int at, int K, float (&x)[VEC])
 {
     typedef typename Elem<T>::type E;
-    typedef E EN __attribute__((ext_vector_type(N), aligned(N == 1 ? sizeof(E) : 16)));
-    const EN v = *reinterpret_cast<const EN *>(reinterpret_cast<const E *>(p) + at);
+    typedef E EN __attribute__((ext_vector_type(VEC), aligned(sizeof(E))));
+    const E *const q = reinterpret_cast<const E *>(p) + row + at;
+    if (WHOLE || at + VEC <= K) {
+        const EN v = *reinterpret_cast<const EN *>(q);
 #pragma unroll
-    for (int j = 0; j < N; j++)
-        x[j] = (float)v[j];
+        for (int j = 0; j < VEC; j++)
+            x[j] = (float)v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j++)
+            x[j] = at + j < K ? (float)q[j] : 0.0f;
+    }
 }
-template <int T, int N>
-__device__ __forceinline__ void store_n(void *p, int64_t at, const float (&x)[N])
+template <int T, bool WHOLE>
+__device__ __forceinline__ void store_n(void *p, int64_t row, int at, int K, const float (&x)[VEC])
 {
     typedef typename Elem<T>::type E;
-    typedef E EN __attribute__((ext_vector_type(N), aligned(N == 1 ? sizeof(E) : 16)));
+    typedef E EN __attribute__((ext_vector_type(VEC), aligned(sizeof(E))));
+    E *const q = reinterpret_cast<E *>(p) + row + at;
     EN v;
 #pragma unroll
-    for (int j = 0; j < N; j++)
+    for (int j = 0; j < VEC; j++)
         v[j] = (E)x[j];
-    *reinterpret_cast<EN *>(reinterpret_cast<E *>(p) + at) = v;
+    if (WHOLE || at + VEC <= K) {
+        *reinterpret_cast<EN *>(q) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j++)
+            if (at + j < K)
+                q[j] = v[j];
+    }
 }
 
-// The weights of a thread's N elements, of any type.
-template <int N>
-__device__ __forceinline__ void load_weight(int type, const void *p, int at, float (&w)[N])
+// Weights, of any type.
+template <bool WHOLE>
+__device__ __forceinline__ void load_weight(const NormArgs &A, int at, float (&w)[VEC])
 {
-    if (type == PN_F32)
-        load_n<PN_F32, N>(p, at, w);
-    else if (type == PN_BF16)
-        load_n<PN_BF16, N>(p, at, w);
+    if (A.weight_type == PN_F32)
+        load_n<PN_F32, WHOLE>(A.weight, 0, at, A.K, w);
+    else if (A.weight_type == PN_BF16)
+        load_n<PN_BF16, WHOLE>(A.weight, 0, at, A.K, w);
     else
-        load_n<PN_F16, N>(p, at, w);
+        load_n<PN_F16, WHOLE>(A.weight, 0, at, A.K, w);
 }
 
-__device__ __forceinline__ double wave_sum64(double v)
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+constexpr uint32_t kInf = 0x7F800000u;  // magnitudes from here on are not finite
+
+// What a row's lanes have found: the sum of squares, the largest |t| and its bits in fp32, numbers that are not finite.
+struct Found {
+    double ss, top;
+    uint32_t bits;
+    int bad;
+};
+
+// The same for all lanes of the row; `lds` is free where `again`.
+template <bool WAVE>
+__device__ __forceinline__ Found over_row(Found f, Found (&lds)[16], bool again)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v += __shfl_xor(v, o, 64);
-    return v;
-}
-__device__ __forceinline__ double wave_max64(double v)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v = fmax(v, __shfl_xor(v, o, 64));
-    return v;
+    f.ss = over_lanes_sum(f.ss);
+    f.top = over_lanes_max(f.top);
+    f.bits = over_lanes_max(f.bits);
+    f.bad = __any(f.bad);
+    if constexpr (!WAVE) {
+        if (again)
+            __syncthreads();
+        if ((threadIdx.x & 63) == 0)
+            lds[threadIdx.x >> 6] = f;
+        __syncthreads();
+        // sixteen lanes have sixteen waves
+        const int v = threadIdx.x & 15;
+        f = v < (int)blockDim.x >> 6 ? lds[v] : Found{0.0, 0.0, 0, 0};
+        const auto join = [&](auto mask) {
+            constexpr int M = mask.value;
+            f.ss += __builtin_bit_cast(double, moved_by<M>(__builtin_bit_cast(u64, f.ss)));
+            f.top = fmax(f.top, __builtin_bit_cast(double, moved_by<M>(__builtin_bit_cast(u64, f.top))));
+            f.bits = max(f.bits, moved_by<M>(f.bits));
+        };
+        join(std::integral_constant<int, 1>());
+        join(std::integral_constant<int, 2>());
+        join(std::integral_constant<int, 4>());
+        join(std::integral_constant<int, 8>());
+        f.bad = __any(f.bad);
+    }
+    return f;
 }
 
-// rint((127 t) / T): `t` and `inv` = 127 / T in fp32 where that is enough, `exact` gives t in 64 bits.
-template <typename F>
-__device__ __forceinline__ int code_of(float t, float inv, bool plain, double T, F exact)
-{
-    const float c = t * inv, n = rintf(c);
-    int code = (int)n;
-    if (!plain || !(fabsf(c - n) < 0.4999f))
-        code = (int)rint((127.0 * exact()) / T);
-    return code;
-}
+enum { ROWS_ONLY, NORM_SHORT, NORM_LONG };
 
-// NORM: the norm with a weight; else the numbers' 8-bit rows alone. VEC: elements a load (8, or 1 for rows
-// that are not aligned). NV: pieces of VEC elements a thread holds. WAVE: a wave a row.
-template <int T, bool NORM, int VEC, int NV, bool WAVE>
+// MODE: the numbers' 8-bit rows alone, or the norm with products that are exact in fp32 or (LONG) may not be. NV: pieces
+// of VEC elements a thread holds. WAVE: a wave a row. WHOLE: K is a multiple of VEC.
+template <int T, int MODE, int NV, bool WAVE, bool WHOLE>
 __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
 {
-    __shared__ double lds[2][16];
-    __shared__ int lds_bad[16];
+    __shared__ Found lds[16];
+    constexpr bool NORM = MODE != ROWS_ONLY;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int threads = WAVE ? 64 : (int)blockDim.x, thread = WAVE ? lane : (int)threadIdx.x;
     const int64_t row = WAVE ? (int64_t)blockIdx.x * (blockDim.x >> 6) + wave : (int64_t)blockIdx.x;
@@ -103,12 +142,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
         return;
 
     float h[NV][VEC];
-    double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int at = (i * threads + thread) * VEC;
         if (at < A.K)
-            load_n<T, VEC>(A.x, row * A.x_stride + at, h[i]);
+            load_n<T, WHOLE>(A.x, row * A.x_stride, at, A.K, h[i]);
     }
     if (NORM && A.residual) {
 #pragma unroll
@@ -116,7 +154,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
             const int at = (i * threads + thread) * VEC;
             if (at < A.K) {
                 float r[VEC];
-                load_n<T, VEC>(A.residual, row * A.residual_stride + at, r);
+                load_n<T, WHOLE>(A.residual, row * A.residual_stride, at, A.K, r);
 #pragma unroll
                 for (int j = 0; j < VEC; j++)
                     h[i][j] = (float)(typename Elem<T>::type)(h[i][j] + r[j]);
@@ -126,8 +164,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
     // the weights stay in registers where there is room, else they are read again (from the caches)
     constexpr bool HOLD = NV * VEC <= 32;
     float held[HOLD ? NV : 1][VEC];
-    double top = 0.0;
-    bool bad = false;
+    Found f{0.0, 0.0, 0, 0};
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int at = (i * threads + thread) * VEC;
@@ -136,47 +173,60 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
         float (&w)[VEC] = held[HOLD ? i : 0];
         if constexpr (NORM) {
             if (A.sum)
-                store_n<T, VEC>(A.sum, row * A.sum_stride + at, h[i]);
-            load_weight<VEC>(A.weight_type, A.weight, at, w);
+                store_n<T, WHOLE>(A.sum, row * A.sum_stride, at, A.K, h[i]);
+            load_weight<WHOLE>(A, at, w);
         }
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
             if constexpr (NORM) {
                 const double d = (double)h[i][j];
-                ss = fma(d, d, ss);
-                top = fmax(top, fabs(d * (double)w[j]));
-                bad |= !(fabsf(w[j]) <= FLT_MAX);
-            } else {
-                top = fmax(top, (double)fabsf(h[i][j]));
+                f.ss = fma(d, d, f.ss);
             }
-            bad |= !(fabsf(h[i][j]) <= FLT_MAX);
+            if constexpr (MODE == ROWS_ONLY)
+                f.bits = max(f.bits, magnitude(h[i][j]));
+            if constexpr (MODE == NORM_SHORT)
+                f.bits = max(f.bits, magnitude(h[i][j] * w[j]));
+            if constexpr (MODE == NORM_LONG) {
+                f.top = fmax(f.top, fabs((double)h[i][j] * (double)w[j]));
+                f.bad |= magnitude(h[i][j]) >= kInf || magnitude(w[j]) >= kInf;
+            }
         }
     }
-    top = wave_max64(top);
-    if constexpr (NORM)
-        ss = wave_sum64(ss);
-    int any = __any(bad);
-    if constexpr (!WAVE) {
-        if (lane == 0) {
-            lds[0][wave] = top;
-            lds[1][wave] = ss;
-            lds_bad[wave] = any;
-        }
-        __syncthreads();
-        top = ss = 0.0;
-        any = 0;
-        for (int v = 0; v < (int)blockDim.x >> 6; v++) {
-            top = fmax(top, lds[0][v]);
-            ss += lds[1][v];
-            any |= lds_bad[v];
-        }
+    f = over_row<WAVE>(f, lds, false);
+    double top = f.top;
+    int none = f.bad;
+    if constexpr (MODE != NORM_LONG) {
+        top = (double)__builtin_bit_cast(float, f.bits);
+        none = f.bits >= kInf;
     }
-    const double r = NORM ? 1.0 / sqrt(ss / A.K + (double)A.eps) : 1.0;
-    const bool none = any || !(r < INFINITY);  // no finite numbers in the row
-    const float inv = (float)(127.0 / top);
-    const bool plain = top > 0x1p-100 && top < 0x1p100;
+    // fp32 products that passed its range, or fell below it
+    if (MODE == NORM_SHORT && !(top > 0x1p-100 && top < 0x1p100)) {
+        Found g{0.0, 0.0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int at = (i * threads + thread) * VEC;
+            if (at >= A.K)
+                continue;
+            float w[VEC];
+            load_weight<WHOLE>(A, at, w);
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+                g.top = fmax(g.top, fabs((double)h[i][j] * (double)w[j]));
+                g.bad |= magnitude(h[i][j]) >= kInf || magnitude(w[j]) >= kInf;
+            }
+        }
+        g = over_row<WAVE>(g, lds, true);
+        top = g.top;
+        none = g.bad;
+    }
+
+    double r = 1.0;
+    if (NORM && (A.out || thread == 0))
+        r = 1.0 / sqrt(f.ss / A.K + (double)A.eps);
     if (A.scales && thread == 0)
-        A.scales[row] = none ? __builtin_nanf("") : (float)(top * r / 127.0);
+        A.scales[row] = none || !(r < INFINITY) ? __builtin_nanf("") : (float)(top * r / 127.0);
+    const bool zero = none || !(top > 0.0), plain = top > 0x1p-100 && top < 0x1p100;
+    const float inv = plain ? 127.0f / (float)top : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int at = (i * threads + thread) * VEC;
@@ -185,83 +235,94 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
         float (&w)[VEC] = held[HOLD ? i : 0];
         if constexpr (NORM) {
             if (!HOLD)
-                load_weight<VEC>(A.weight_type, A.weight, at, w);
+                load_weight<WHOLE>(A, at, w);
             if (A.out) {
                 float y[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; j++)
                     y[j] = to_f32((double)h[i][j] * r * (double)w[j]);
-                store_n<T, VEC>(A.out, row * A.out_stride + at, y);
+                store_n<T, WHOLE>(A.out, row * A.out_stride, at, A.K, y);
             }
         }
         if (A.codes) {
-            int c[VEC];
+            uint32_t c[VEC];  // a code in the low byte of each
+            float worst = 0.0f;
 #pragma unroll
             for (int j = 0; j < VEC; j++) {
-                const float t = NORM ? h[i][j] * w[j] : h[i][j];
-                c[j] = none || !(top > 0.0) ? 0 : code_of(t, inv, plain, top, [&] {
-                    return NORM ? (double)h[i][j] * (double)w[j] : (double)h[i][j];
-                });
+                // the sum with 1.5 * 2^23 has the nearest whole number in its low bits
+                const float q = (NORM ? h[i][j] * w[j] : h[i][j]) * inv, n = q + 0x1.8p23f;
+                worst = fmaxf(worst, fabsf(q - (n - 0x1.8p23f)));
+                c[j] = __builtin_bit_cast(uint32_t, n);
+            }
+            if (zero) {
+#pragma unroll
+                for (int j = 0; j < VEC; j++)
+                    c[j] = 0;
+            } else if (!plain || !(worst < 0.49995f)) {
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    const double t = NORM ? (double)h[i][j] * (double)w[j] : (double)h[i][j];
+                    c[j] = (uint32_t)(int)rint((127.0 * t) / top);
+                }
             }
             int8_t *const p = A.codes + row * A.K + at;
-            if constexpr (VEC == 8) {
-                uint2 b = make_uint2(0, 0);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    b.x |= ((uint32_t)c[j] & 255u) << (8 * j);
-                    b.y |= ((uint32_t)c[4 + j] & 255u) << (8 * j);
-                }
-                *reinterpret_cast<uint2 *>(p) = b;
+            if (WHOLE || at + VEC <= A.K) {
+                const auto four = [&](int j) {
+                    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[j + 3], c[j + 2], 0x0c0c0400u),
+                                                 __builtin_amdgcn_perm(c[j + 1], c[j], 0x0c0c0400u), 0x05040100u);
+                };
+                typedef uint32_t u32x2a1 __attribute__((ext_vector_type(2), aligned(1)));
+                *reinterpret_cast<u32x2a1 *>(p) = u32x2a1{four(0), four(4)};
             } else {
-                *p = (int8_t)c[0];
+#pragma unroll
+                for (int j = 0; j < VEC; j++)
+                    if (at + j < A.K)
+                        p[j] = (int8_t)c[j];
             }
         }
     }
 }
 
-template <int T, bool NORM, int VEC, int NV, bool WAVE>
-static void launch_norm(const NormArgs &A, int threads, hipStream_t s)
+template <int T, int MODE, int NV, bool WAVE>
+static void launch_norm(const NormArgs &A, int pieces, hipStream_t s)
 {
-    const int per = WAVE ? 4 : 1;
-    hipLaunchKernelGGL((norm_kernel<T, NORM, VEC, NV, WAVE>), dim3((unsigned)((A.rows + per - 1) / per)),
-                       dim3(WAVE ? 256 : threads), 0, s, A);
+    const int per = WAVE ? 4 : 1, threads = ((pieces + NV - 1) / NV + 63) / 64 * 64;
+    const dim3 grid((unsigned)((A.rows + per - 1) / per)), block(WAVE ? 256 : threads);
+    if (A.K % VEC == 0)
+        hipLaunchKernelGGL((norm_kernel<T, MODE, NV, WAVE, true>), grid, block, 0, s, A);
+    else
+        hipLaunchKernelGGL((norm_kernel<T, MODE, NV, WAVE, false>), grid, block, 0, s, A);
 }
 
-template <int T, bool NORM>
-static int run_norm(const NormArgs &A, bool vec, hipStream_t s)
+// A thread holds one piece where rows are few, for latency, or of fp32 (8192 rows of 5120, norm: one 120 us, two 128), and
+// else two up to 8192 elements (bf16: one 72 us, two 63, four 72), four up to 32768.
+template <int T, int MODE>
+static int run_norm(const NormArgs &A, hipStream_t s)
 {
-    const auto wide = [](int pieces, int nv) { return ((pieces + nv - 1) / nv + 63) / 64 * 64; };
-    if (vec) {
-        const int pieces = A.K / 8;
-        if (pieces <= 64)
-            launch_norm<T, NORM, 8, 1, true>(A, 0, s);
-        else if (pieces <= 128)
-            launch_norm<T, NORM, 8, 2, true>(A, 0, s);
-        else if (pieces <= 512)
-            launch_norm<T, NORM, 8, 1, false>(A, wide(pieces, 1), s);
-        else if (pieces <= 1024)
-            launch_norm<T, NORM, 8, 2, false>(A, wide(pieces, 2), s);
-        else if (pieces <= 4096)
-            launch_norm<T, NORM, 8, 4, false>(A, wide(pieces, 4), s);
-        else
-            launch_norm<T, NORM, 8, 8, false>(A, wide(pieces, 8), s);
-    } else {
-        if (A.K <= 512)
-            launch_norm<T, NORM, 1, 8, true>(A, 0, s);
-        else if (A.K <= 8192)
-            launch_norm<T, NORM, 1, 8, false>(A, wide(A.K, 8), s);
-        else
-            launch_norm<T, NORM, 1, 64, false>(A, wide(A.K, 64), s);
-    }
+    const int pieces = (A.K + VEC - 1) / VEC;
+    if (pieces <= 64)
+        launch_norm<T, MODE, 1, true>(A, pieces, s);
+    else if (pieces <= 128)
+        launch_norm<T, MODE, 2, true>(A, pieces, s);
+    else if (pieces <= (T == PN_F32 || A.rows < 256 ? 1024 : 512))
+        launch_norm<T, MODE, 1, false>(A, pieces, s);
+    else if (pieces <= 1024)
+        launch_norm<T, MODE, 2, false>(A, pieces, s);
+    else if (pieces <= 4096)
+        launch_norm<T, MODE, 4, false>(A, pieces, s);
+    else
+        launch_norm<T, MODE, 8, false>(A, pieces, s);
     return launch_status();
 }
 
-template <bool NORM>
-static int by_type(int type, const NormArgs &A, bool vec, hipStream_t s)
+// Products of two 16-bit numbers are exact in fp32.
+static int run_norm_of(int type, const NormArgs &A, hipStream_t s)
 {
-    return type == PN_F32    ? run_norm<PN_F32, NORM>(A, vec, s)
-           : type == PN_BF16 ? run_norm<PN_BF16, NORM>(A, vec, s)
-                             : run_norm<PN_F16, NORM>(A, vec, s);
+    const bool is_short = A.weight_type != PN_F32;
+    return type == PN_F32    ? run_norm<PN_F32, NORM_LONG>(A, s)
+           : type == PN_BF16 ? is_short ? run_norm<PN_BF16, NORM_SHORT>(A, s) : run_norm<PN_BF16, NORM_LONG>(A, s)
+           : is_short        ? run_norm<PN_F16, NORM_SHORT>(A, s)
+                             : run_norm<PN_F16, NORM_LONG>(A, s);
 }
 
 // Rows and widths that the kernels take.
@@ -269,9 +330,6 @@ static bool rows_fit(int64_t rows, int64_t K)
 {
     return rows >= 0 && rows <= INT32_MAX && K >= 1 && K <= PN_ROW_MAX_WIDTH;
 }
-
-// Whether rows of `size`-byte elements at p take loads of eight elements (16-byte pieces).
-static bool eights(const void *p, int64_t stride, int size) { return aligned(p, 16) && (stride * size & 15) == 0; }
 
 }  // namespace pn
 
@@ -301,7 +359,10 @@ extern "C" int pn_int8_quantize_rows(int type, const void *x, int64_t x_stride, 
     A.x_stride = x_stride;
     A.codes = codes;
     A.scales = scales;
-    return by_type<false>(type, A, K % 8 == 0 && eights(x, x_stride, size) && aligned(codes, 8), (hipStream_t)stream);
+    hipStream_t s = (hipStream_t)stream;
+    return type == PN_F32    ? run_norm<PN_F32, ROWS_ONLY>(A, s)
+           : type == PN_BF16 ? run_norm<PN_BF16, ROWS_ONLY>(A, s)
+                             : run_norm<PN_F16, ROWS_ONLY>(A, s);
 }
 
 extern "C" int pn_add_norm(const pn_add_norm_args *a, void *stream)
@@ -325,10 +386,5 @@ extern "C" int pn_add_norm(const pn_add_norm_args *a, void *stream)
         return st;
     const NormArgs A{a->rows, a->x_stride, a->residual_stride, a->sum_stride, a->out_stride, (int)a->K,
                      a->x, a->residual, a->weight, a->sum, a->out, a->codes, a->scales, a->weight_type, a->eps};
-    const bool vec = a->K % 8 == 0 && eights(a->x, a->x_stride, size) &&
-                     (!a->residual || eights(a->residual, a->residual_stride, size)) &&
-                     (!a->sum || eights(a->sum, a->sum_stride, size)) &&
-                     (!a->out || eights(a->out, a->out_stride, size)) && aligned(a->weight, 16) &&
-                     aligned(a->codes, 8);
-    return by_type<true>(a->type, A, vec, (hipStream_t)stream);
+    return run_norm_of(a->type, A, (hipStream_t)stream);
 }
