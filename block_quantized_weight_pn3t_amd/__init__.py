@@ -385,7 +385,12 @@ class _Torch:
         import torch
         cls.i32, cls.i64, cls.u8, cls.i8 = torch.int32, torch.int64, torch.uint8, torch.int8
         cls.kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-        cls.stream = torch.cuda.current_stream
+        cls.device = torch.cuda.current_device if torch.cuda.is_available() else lambda: None
+        cls.raw_stream = lambda device: torch.cuda.current_stream().cuda_stream
+        if torch.cuda.is_available() and hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            # the same without the objects in between, which take as long as a launch
+            torch.cuda.init()
+            cls.device, cls.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         cls.f32 = torch.float32
         return cls
 
@@ -414,7 +419,7 @@ def _elem(t, name, T):
 
 
 def _handle(stream, T):
-    return T.stream().cuda_stream if stream is None else _stream(stream)
+    return T.raw_stream(T.device()) if stream is None else _stream(stream)
 
 
 def cache_page_bytes(format, heads, dim, page):
@@ -599,45 +604,60 @@ def verify(p, q, draft, u_accept, u_sample, tokens, accepted, workspace, n_draft
 
 
 # ---- a prompt's norm, 8-bit products, rotated keys, log probabilities -----------------------------
+#
+# As above; every tensor has to be on the current device, whose stream the call goes to.
 
-def _rows(t, name, dtype, rows, width):
-    """The spacing of the rows of t [rows, width], of `dtype` on the device."""
-    if t.dtype is not dtype or t.shape != (rows, width) or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor of {dtype} [{rows}, {width}], got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _misfit(t, name, dtype, shape, dev, how):
+    """Says what is wrong with a tensor that is not what it has to be."""
+    raise ValueError(f"{name} must be {how} of {dtype} {tuple(shape)} on the current device ({dev}), got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _flat(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _misfit(t, name, dtype, shape, dev, "a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, dev, written=False):
+    """The spacing of the rows of t [rows, width]; rows that are written must not overlap."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _misfit(t, name, dtype, shape, dev, "rows")
     row, column = t.stride()
-    if column != 1 and width > 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
+    if (column != 1 and shape[1] > 1) or (written and row < shape[1] and shape[0] > 1):
+        _misfit(t, name, dtype, shape, dev, "contiguous rows" + " that do not overlap" * written)
     return row
 
 
-def _written_rows(t, name, dtype, rows, width):
-    """The same for rows that are written: they must not overlap."""
-    row = _rows(t, name, dtype, rows, width)
-    if rows > 1 and abs(row) < width:
-        raise ValueError(f"the rows of {name} overlap")
-    return row
+def _plain_kind(t, name, dim, dev, T):
+    """The element type id of a plain tensor of `dim` dimensions."""
+    kind = T.kinds.get(t.dtype)
+    if kind is None or t.dim() != dim or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor of {dim} dimensions of float32, bfloat16 or float16 on the current "
+                         f"device ({dev}), got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return kind
 
 
-def _codes(codes, scales, rows, width, T):
-    if not _is(codes, T.i8, (rows, width)):
-        _refuse(codes, "codes", T.i8, (rows, width))
-    if not _is(scales, T.f32, (rows,)):
-        _refuse(scales, "scales", T.f32, (rows,))
+def _workspace(t, dev, T):
+    """A workspace's address and bytes."""
+    if t is None:
+        return 0, 0
+    n = t.numel()
+    return _flat(t, "workspace", T.u8, (n,), dev), n
 
 
 def int8_quantize_rows(x, codes, scales, stream=None):
     """codes int8[N, K] and scales fp32[N] <- the rows of x [N, K] as 8-bit integers with one scale each
     (pn_int8_quantize_rows): activations before gemm_int8, and its weights."""
     T = _names()
-    kind = _elem(x, "x", T)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [N, K], got {tuple(x.shape)}")
-    n, k = x.shape
-    row = _rows(x, "x", x.dtype, n, k)
-    _codes(codes, scales, n, k, T)
-    _check(_lib.pn_int8_quantize_rows(kind, x.data_ptr(), row, n, k, codes.data_ptr(), scales.data_ptr(),
-                                      _handle(stream, T)), "pn_int8_quantize_rows")
+    dev = T.device()
+    kind = _plain_kind(x, "x", 2, dev, T)
+    shape = n, k = x.shape
+    row = _rows(x, "x", x.dtype, shape, dev)
+    codes_at, scales_at = _flat(codes, "codes", T.i8, shape, dev), _flat(scales, "scales", T.f32, (n,), dev)
+    _check(_lib.pn_int8_quantize_rows(kind, x.data_ptr(), row, n, k, codes_at, scales_at, _handle(stream, T)),
+           "pn_int8_quantize_rows")
 
 
 _pack_add_norm = struct.Struct("@iiqqPqPqPqPfPqPP").pack  # pn_add_norm_args
@@ -648,31 +668,28 @@ def add_norm(x, weight, eps, out=None, codes=None, scales=None, residual=None, s
     numbers of x's type, codes int8[N, K] and scales fp32[N] <- 8-bit rows for gemm_int8; either or both.
     sum [N, K] <- x + residual, which the norm is of; sum and out may be x or residual themselves."""
     T = _names()
-    kind = _elem(x, "x", T)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [N, K], got {tuple(x.shape)}")
-    n, k = x.shape
+    dev = T.device()
+    kind = _plain_kind(x, "x", 2, dev, T)
+    shape = n, k = x.shape
     dt = x.dtype
-    x_row = _rows(x, "x", dt, n, k)
-    weight_kind = _elem(weight, "weight", T)
-    if not _is(weight, weight.dtype, (k,)):
-        _refuse(weight, "weight", weight.dtype, (k,))
+    x_row = _rows(x, "x", dt, shape, dev)
+    weight_kind = _plain_kind(weight, "weight", 1, dev, T)
+    weight_at = _flat(weight, "weight", weight.dtype, (k,), dev)
     residual_at = residual_row = sum_at = sum_row = out_at = out_row = codes_at = scales_at = 0
     if residual is not None:
-        residual_row, residual_at = _rows(residual, "residual", dt, n, k), residual.data_ptr()
+        residual_row, residual_at = _rows(residual, "residual", dt, shape, dev), residual.data_ptr()
     if sum is not None:
-        sum_row, sum_at = _written_rows(sum, "sum", dt, n, k), sum.data_ptr()
+        sum_row, sum_at = _rows(sum, "sum", dt, shape, dev, True), sum.data_ptr()
     if out is not None:
-        out_row, out_at = _written_rows(out, "out", dt, n, k), out.data_ptr()
+        out_row, out_at = _rows(out, "out", dt, shape, dev, True), out.data_ptr()
     if codes is not None or scales is not None:
         if codes is None or scales is None:
             raise ValueError("codes and scales go together")
-        _codes(codes, scales, n, k, T)
-        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
+        codes_at, scales_at = _flat(codes, "codes", T.i8, shape, dev), _flat(scales, "scales", T.f32, (n,), dev)
     elif out is None:
         raise ValueError("out, or codes and scales, must be given")
     a = _pack_add_norm(kind, weight_kind, n, k, x.data_ptr(), x_row, residual_at, residual_row, sum_at, sum_row,
-                       weight.data_ptr(), eps, out_at, out_row, codes_at, scales_at)
+                       weight_at, eps, out_at, out_row, codes_at, scales_at)
     _check(_lib.pn_add_norm(a, _handle(stream, T)), "pn_add_norm")
 
 
@@ -686,34 +703,28 @@ def gemm_int8(a, a_scales, w, w_scales, out, workspace=None, stream=None):
     int8[N, K], rows scaled by a_scales fp32[M] and w_scales fp32[N] (pn_gemm_int8). workspace: a uint8
     tensor of gemm_int8_workspace_bytes."""
     T = _names()
-    kind = _elem(out, "out", T)
+    dev = T.device()
+    kind = _plain_kind(out, "out", 2, dev, T)
     if a.dim() != 2 or w.dim() != 2:
         raise ValueError(f"a and w must be [M, K] and [N, K], got {tuple(a.shape)} and {tuple(w.shape)}")
     m, k = a.shape
     n = w.shape[0]
-    if not _is(a, T.i8, (m, k)):
-        _refuse(a, "a", T.i8, (m, k))
-    if not _is(w, T.i8, (n, k)):
-        _refuse(w, "w", T.i8, (n, k))
-    if not _is(a_scales, T.f32, (m,)):
-        _refuse(a_scales, "a_scales", T.f32, (m,))
-    if not _is(w_scales, T.f32, (n,)):
-        _refuse(w_scales, "w_scales", T.f32, (n,))
-    row = _written_rows(out, "out", out.dtype, m, n)
-    work_at = work_bytes = 0
-    if workspace is not None:
-        _dev(workspace, "workspace", T.u8)
-        work_at, work_bytes = workspace.data_ptr(), workspace.numel()
-    _check(_lib.pn_gemm_int8(a.data_ptr(), a_scales.data_ptr(), m, w.data_ptr(), w_scales.data_ptr(), n, k, kind,
-                             out.data_ptr(), row, work_at, work_bytes, _handle(stream, T)), "pn_gemm_int8")
+    a_at, w_at = _flat(a, "a", T.i8, (m, k), dev), _flat(w, "w", T.i8, (n, k), dev)
+    a_scales_at = _flat(a_scales, "a_scales", T.f32, (m,), dev)
+    w_scales_at = _flat(w_scales, "w_scales", T.f32, (n,), dev)
+    row = _rows(out, "out", out.dtype, (m, n), dev, True)
+    work_at, work_bytes = _workspace(workspace, dev, T)
+    _check(_lib.pn_gemm_int8(a_at, a_scales_at, m, w_at, w_scales_at, n, k, kind, out.data_ptr(), row, work_at,
+                             work_bytes, _handle(stream, T)), "pn_gemm_int8")
 
 
-def _heads(t, name, dtype, shape):
+def _heads(t, name, dtype, shape, dev):
     """The token and head strides of t [T, heads, dim], channels contiguous."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or t.stride(2) != 1:
-        raise ValueError(f"{name} must be a device tensor of {dtype} {tuple(shape)} with contiguous channels, got "
-                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.stride(0), t.stride(1)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        token, head, channel = t.stride()
+        if channel == 1:
+            return token, head
+    _misfit(t, name, dtype, shape, dev, "a tensor with contiguous channels")
 
 
 _pack_append = struct.Struct("@iiPqqPqqPqqPqqPqiiPPq").pack  # pn_append_args
@@ -725,33 +736,31 @@ def cache_append(cache, k, v, slots, rotation, positions=None, q=None, q_out=Non
     sines of each position for the first rot channels of a head; positions int64[T]: a token's row of it,
     its own number unless given. interleaved: channels (2j, 2j + 1) turn together, not (j, j + rot / 2)."""
     T = _names()
-    kind = _elem(k, "k", T)
+    dev = T.device()
+    kind = _plain_kind(k, "k", 3, dev, T)
     n, dt = k.shape[0], k.dtype
     shape = (n, cache.heads, cache.dim)
-    k_token, k_head = _heads(k, "k", dt, shape)
-    v_token, v_head = _heads(v, "v", dt, shape)
-    if not _is(slots, T.i64, (n,)):
-        _refuse(slots, "slots", T.i64, (n,))
+    k_token, k_head = _heads(k, "k", dt, shape, dev)
+    v_token, v_head = _heads(v, "v", dt, shape, dev)
+    slots_at = _flat(slots, "slots", T.i64, (n,), dev)
     if rotation.dim() != 2:
         raise ValueError(f"rotation must be [positions, rot], got {tuple(rotation.shape)}")
-    if not _is(rotation, T.f32, rotation.shape):
-        _refuse(rotation, "rotation", T.f32, rotation.shape)
     rows, rot = rotation.shape
+    rotation_at = _flat(rotation, "rotation", T.f32, (rows, rot), dev)
     positions_at = hq = q_at = q_token = q_head = out_at = out_token = out_head = 0
     if positions is not None:
-        if not _is(positions, T.i64, (n,)):
-            _refuse(positions, "positions", T.i64, (n,))
-        positions_at = positions.data_ptr()
+        positions_at = _flat(positions, "positions", T.i64, (n,), dev)
     if q is not None:
         if q.dim() != 3 or q_out is None:
             raise ValueError("q must be [T, Hq, dim], with q_out to go to")
         hq = q.shape[1]
-        q_token, q_head = _heads(q, "q", dt, (n, hq, cache.dim))
-        out_token, out_head = _heads(q_out, "q_out", dt, (n, hq, cache.dim))
+        shape = (n, hq, cache.dim)
+        q_token, q_head = _heads(q, "q", dt, shape, dev)
+        out_token, out_head = _heads(q_out, "q_out", dt, shape, dev)
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
     a = _pack_append(kind, hq, q_at, q_token, q_head, out_at, out_token, out_head, k.data_ptr(), k_token, k_head,
-                     v.data_ptr(), v_token, v_head, rotation.data_ptr(), rows, rot, 1 if interleaved else 0,
-                     positions_at, slots.data_ptr(), n)
+                     v.data_ptr(), v_token, v_head, rotation_at, rows, rot, 1 if interleaved else 0, positions_at,
+                     slots_at, n)
     _check(_lib.pn_cache_append(cache.ref, a, _handle(stream, T)), "pn_cache_append")
 
 
@@ -770,33 +779,31 @@ def logprobs(logits, tokens=None, logprob=None, workspace=None, rank=None, entro
     log of the sum of exp(scale * logits), top_ids int32[R, top] and top_logprobs fp32[R, top] <- the likeliest
     tokens: those of them that are given. workspace: a uint8 tensor of logprobs_workspace_bytes."""
     T = _names()
-    kind = _elem(logits, "logits", T)
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [R, V], got {tuple(logits.shape)}")
-    R, V = logits.shape
-    row = _rows(logits, "logits", logits.dtype, R, V)
-    at = []
-    for t, name, dtype in ((tokens, "tokens", T.i32), (logprob, "logprob", T.f32), (rank, "rank", T.i32),
-                           (entropy, "entropy", T.f32), (lse, "lse", T.f32)):
-        if t is not None and not _is(t, dtype, (R,)):
-            _refuse(t, name, dtype, (R,))
-        at.append(0 if t is None else t.data_ptr())
-    if tokens is None and (logprob is not None or rank is not None):
+    dev = T.device()
+    kind = _plain_kind(logits, "logits", 2, dev, T)
+    R, V = shape = logits.shape
+    row = _rows(logits, "logits", logits.dtype, shape, dev)
+    one = (R,)
+    tokens_at = logprob_at = rank_at = entropy_at = lse_at = ids_at = top_at = top = 0
+    if tokens is not None:
+        tokens_at = _flat(tokens, "tokens", T.i32, one, dev)
+    elif logprob is not None or rank is not None:
         raise ValueError("logprob and rank need tokens")
-    top = ids_at = top_at = 0
+    if logprob is not None:
+        logprob_at = _flat(logprob, "logprob", T.f32, one, dev)
+    if rank is not None:
+        rank_at = _flat(rank, "rank", T.i32, one, dev)
+    if entropy is not None:
+        entropy_at = _flat(entropy, "entropy", T.f32, one, dev)
+    if lse is not None:
+        lse_at = _flat(lse, "lse", T.f32, one, dev)
     if top_ids is not None or top_logprobs is not None:
         if top_ids is None or top_logprobs is None or top_ids.dim() != 2:
             raise ValueError("top_ids and top_logprobs must both be [R, top]")
         top = top_ids.shape[1]
-        if not _is(top_ids, T.i32, (R, top)):
-            _refuse(top_ids, "top_ids", T.i32, (R, top))
-        if not _is(top_logprobs, T.f32, (R, top)):
-            _refuse(top_logprobs, "top_logprobs", T.f32, (R, top))
-        ids_at, top_at = top_ids.data_ptr(), top_logprobs.data_ptr()
-    work_at = work_bytes = 0
-    if workspace is not None:
-        _dev(workspace, "workspace", T.u8)
-        work_at, work_bytes = workspace.data_ptr(), workspace.numel()
-    a = _pack_logprobs(kind, top, R, V, row, logits.data_ptr(), at[0], scale, at[1], at[2], at[3], at[4], ids_at,
-                       top_at)
+        ids_at = _flat(top_ids, "top_ids", T.i32, (R, top), dev)
+        top_at = _flat(top_logprobs, "top_logprobs", T.f32, (R, top), dev)
+    work_at, work_bytes = _workspace(workspace, dev, T)
+    a = _pack_logprobs(kind, top, R, V, row, logits.data_ptr(), tokens_at, scale, logprob_at, rank_at, entropy_at,
+                       lse_at, ids_at, top_at)
     _check(_lib.pn_logprobs(a, work_at, work_bytes, _handle(stream, T)), "pn_logprobs")
