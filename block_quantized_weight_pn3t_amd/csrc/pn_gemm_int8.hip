@@ -13,9 +13,12 @@
 //   stream  up to 32 tokens: memory bound, every weight read once. A workgroup has an even share of w's
 //           rows; its waves share each tile of 32 rows by K and run on their own, several loads deep, until
 //           their sums meet in LDS.
-//   tile    tiles of 64 x 64 or 128 x 128, where there are too few of the next for all CUs; K is cut among
-//           workgroups where there are too few of these, too, and the last to arrive adds up (pn_arrive.h).
+//   tile    tiles of 64 x 64 or 128 x 128, where there are too few of the next for all CUs; K is cut into parts
+//           where there are too few of these, too, and a tile's last workgroup adds up (pn_arrive.h). (Even
+//           shares of all tiles' lines for each workgroup were no faster: parts pass the caches by and are slow.)
 //   large   tiles of 256 x 256: matrix bound.
+#include <math.h>
+
 #include <algorithm>
 
 #include "pn_arrive.h"
@@ -212,16 +215,17 @@ __device__ __forceinline__ void tile_of(const GemmArgs &A, int block, int blocks
 }
 
 // SIZE x SIZE outputs a workgroup, a quarter each wave.
-template <int SIZE>
+template <int SIZE, int STAGES_>
 struct Square {
-    static constexpr int STAGE = 2 * SIZE * 128, LOADS = STAGE / 4096, STAGES = 4;
+    static constexpr int STAGE = 2 * SIZE * 128, LOADS = STAGE / 4096, STAGES = STAGES_;
     static constexpr int BYTES = STAGES * STAGE, N = SIZE / 32;  // 16-row tiles of a wave, each way
+    static_assert(LOADS == 2 * N);
 };
 
-template <int T, int SIZE>
+template <int T, int SIZE, int STAGES>
 __global__ void __launch_bounds__(256) gemm_int8_tile_kernel(GemmArgs A)
 {
-    typedef Square<SIZE> S;
+    typedef Square<SIZE, STAGES> S;
     typedef typename Elem<T>::type E;
     typedef E E4 __attribute__((ext_vector_type(4)));
     extern __shared__ i32x4_t lds[];  // [stage][a, w][row][piece]
@@ -236,52 +240,71 @@ __global__ void __launch_bounds__(256) gemm_int8_tile_kernel(GemmArgs A)
     const int r = threadIdx.x >> 3, piece = (lane & 7) ^ (r & 7);
     const int8_t *const a0 = A.a + m0 * A.K, *const w0 = A.w + n0 * A.K;
     const int last_a = (int)min(A.M - 1 - m0, (int64_t)SIZE - 1), last_w = (int)min(A.N - 1 - n0, (int64_t)SIZE - 1);
-    uint32_t src[2][SIZE / 32];
+    uint32_t src[2][S::N];
 #pragma unroll
-    for (int j = 0; j < SIZE / 32; j++) {
+    for (int j = 0; j < S::N; j++) {
         src[0][j] = (uint32_t)(min(r + 32 * j, last_a) * A.K + 16 * piece);
         src[1][j] = (uint32_t)(min(r + 32 * j, last_w) * A.K + 16 * piece);
     }
     const uint32_t stages = (uint32_t)(uintptr_t)lds + wave * 1024;
     const int first = part * A.each, end = min((A.K + 127) / 128, first + A.each);
-    const auto load = [&](int step, int stage) {
-        const int64_t k = step * 128;
-        const bool in = step < end && k + 16 * piece < A.K;
-#pragma unroll
-        for (int o = 0; o < 2; o++)
-#pragma unroll
-            for (int j = 0; j < SIZE / 32; j++)
-                load_lds(in ? (o ? w0 : a0) + k + src[o][j] : reinterpret_cast<const int8_t *>(kZeros),
-                         stages + stage * S::STAGE + o * SIZE * 128 + j * 4096);
+    // load n of a step: the first half of them are a's rows
+    const auto load = [&](int step, int stage, int n) {
+        const int k = step < end ? step * 128 : A.K, o = n / S::N, j = n % S::N;
+        const bool in = k + 16 * piece < A.K;
+        load_lds(in ? (o ? w0 : a0) + k + src[o][j] : reinterpret_cast<const int8_t *>(kZeros),
+                 stages + stage * S::STAGE + o * SIZE * 128 + j * 4096);
     };
 #pragma unroll
-    for (int i = 0; i < S::STAGES - 1; i++)
-        load(first + i, i);
+    for (int i = 0; i < S::STAGES; i++)
+#pragma unroll
+        for (int n = 0; n < S::LOADS; n++)
+            load(first + i, i, n);
     const int row = lane & 15, g = lane >> 4, wm = (wave & 1) * (SIZE / 2), wn = (wave >> 1) * (SIZE / 2);
     const uint32_t first_a = (wm + row) * 128 + (g ^ (lane & 7)) * 16, first_w = (SIZE + wn + row) * 128 + (g ^ (lane & 7)) * 16;
-    i32x4_t acc[S::N][S::N] = {};  // [16 of m][16 of n]
-    int stage = 0, next = S::STAGES - 1;
-    for (int step = first; step < end; step++) {
-        wait<(S::STAGES - 2) * S::LOADS, true>();  // this step has landed, the last one has been read
-        barrier();
-        load(step + S::STAGES - 1, next);
+    i32x4_t fa[2][S::N][2], fw[2][S::N][2];  // [step & 1]: one is read while the other is multiplied
+    const auto read = [&](int stage, int to, int i, int t) {
         const char *const p = base + stage * S::STAGE;
+        fa[to][i][t] = *reinterpret_cast<const i32x4_t *>(p + (first_a ^ 64 * t) + i * 2048);
+        fw[to][i][t] = *reinterpret_cast<const i32x4_t *>(p + (first_w ^ 64 * t) + i * 2048);
+    };
+    i32x4_t acc[S::N][S::N] = {};  // [16 of m][16 of n]
+    wait<(S::STAGES - 1) * S::LOADS, true>();
+    barrier();
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            i32x4_t fa[S::N], fw[S::N];
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int i = 0; i < S::N; i++)
+            read(0, 0, i, t);
+    int stage = 0;
+    const auto one = [&](int step, int from) {
+        wait<(S::STAGES - 2) * S::LOADS, true>();  // the next step has landed, this one has been read
+        barrier();
+        const int to = stage;
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+        // one wave a SIMD: products, reads of the next step and loads in turn keep all three under way
+#pragma unroll
+        for (int t = 0; t < 2; t++)
 #pragma unroll
             for (int i = 0; i < S::N; i++) {
-                fa[i] = *reinterpret_cast<const i32x4_t *>(p + (first_a ^ 64 * t) + i * 2048);
-                fw[i] = *reinterpret_cast<const i32x4_t *>(p + (first_w ^ 64 * t) + i * 2048);
-            }
-#pragma unroll
-            for (int i = 0; i < S::N; i++)
+                read(stage, from ^ 1, i, t);
+                load(step + S::STAGES, to, t * S::N + i);
 #pragma unroll
                 for (int j = 0; j < S::N; j++)
-                    acc[i][j] = products(fw[j], fa[i], acc[i][j]);
-        }
-        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-        next = next + 1 == S::STAGES ? 0 : next + 1;
+                    acc[i][j] = products(fw[from][j][t], fa[from][i][t], acc[i][j]);
+                order();
+            }
+        // (used here, or the compiler moves the reads to where the next step begins)
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int i = 0; i < S::N; i++)
+                asm volatile("" : "+v"(fa[from ^ 1][i][t]), "+v"(fw[from ^ 1][i][t]));
+    };
+    for (int step = first; step < end; step += 2) {
+        one(step, 0);
+        if (step + 1 < end)
+            one(step + 1, 1);
     }
     wait<0, true>();
     if (A.splits > 1) {
@@ -552,22 +575,36 @@ struct GemmCut {
 static GemmCut gemm_cut(int64_t M, int64_t N, int64_t K)
 {
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    const auto tiles = [&](int size) { return up(M, size) * up(N, size); };
     const int64_t cus = device_cus(), lines = up(K, 128);
     GemmCut c = {};
     c.splits = 1;
     c.each = (int)lines;
     if (M <= 32)
         return c;
-    c.size = tiles(256) >= cus * 3 / 4 ? 256 : tiles(128) >= cus ? 128 : 64;
-    if (c.size == 64) {
-        const int64_t t = tiles(64);
-        // two workgroups a CU, each with at least eight lines
-        c.splits = (int)std::max<int64_t>(1, std::min(2 * cus / t, lines / 8));
-        c.each = (int)up(lines, c.splits);
-        c.splits = (int)up(lines, c.each);
-        if (c.splits > 1)
-            c.workspace = t * kLine * 8 + t * c.splits * 64 * 64 * 4;
+    // What is estimated to be soonest, in us: rounds of workgroups, each some time a line and some to begin and end,
+    // and the joining of K's parts. Measured for a line: 0.25 and 0.38 with one and two workgroups a CU (64), 0.5
+    // (128), 0.92 (256). So 64 x 1024 x 5120 is four parts in tiles of 64 (9.6 us; whole 12.3, in tiles of 128 20), 256 x
+    // 5120 x 17408 three in tiles of 128 (44; 86 whole, 59 in tiles of 64), 1024 x 5120 x 6144 tiles of 128 (57; 60 each
+    // in those of 64 and 256), 2048 x 6144 x 5120 tiles of 256 (61; 92 in those of 128).
+    double best = INFINITY;
+    for (const int size : {64, 128, 256}) {
+        const int64_t t = up(M, size) * up(N, size), slots = size == 64 ? 2 * cus : cus;
+        const double edge = size == 64 ? 1.0 : size == 128 ? 2.0 : 8.5;
+        for (int splits = 1; splits <= (size == 256 ? 1 : std::min<int64_t>(8, lines / 4 + 1)); splits++) {
+            const int64_t each = up(lines, splits), blocks = t * splits;
+            if (up(lines, each) != splits || (splits > 1 && blocks > 2 * slots))
+                continue;
+            const double line = size == 64 ? (blocks <= cus ? 0.25 : 0.38) : size == 128 ? 0.5 : 0.92;
+            const double join = splits == 1 ? 0.0 : size == 64 ? 2.3 + 0.6 * splits : 2.0 + 1.45 * splits;
+            const double time = (double)up(blocks, slots) * ((double)each * line + edge) + join;
+            if (time < best) {
+                best = time;
+                c.size = size;
+                c.splits = splits;
+                c.each = (int)each;
+                c.workspace = splits > 1 ? t * (kLine * 8 + (int64_t)splits * size * size * 4) : 0;
+            }
+        }
     }
     return c;
 }
@@ -599,8 +636,10 @@ static int run_gemm(GemmArgs A, const GemmCut &c, hipStream_t s)
     A.each = c.each;
     const unsigned blocks = (unsigned)A.tiles_m * A.tiles_n * c.splits;
     return c.size == 256   ? launch_gemm<gemm_int8_large_kernel<T>>(A, blocks, 512, kLargeBytes, s)
-           : c.size == 128 ? launch_gemm<gemm_int8_tile_kernel<T, 128>>(A, blocks, 256, Square<128>::BYTES, s)
-                           : launch_gemm<gemm_int8_tile_kernel<T, 64>>(A, blocks, 256, Square<64>::BYTES, s);
+           : c.size == 128 ? launch_gemm<gemm_int8_tile_kernel<T, 128, 4>>(A, blocks, 256, Square<128, 4>::BYTES, s)
+           : blocks <= (unsigned)device_cus()
+               ? launch_gemm<gemm_int8_tile_kernel<T, 64, 8>>(A, blocks, 256, Square<64, 8>::BYTES, s)
+               : launch_gemm<gemm_int8_tile_kernel<T, 64, 4>>(A, blocks, 256, Square<64, 4>::BYTES, s);
 }
 
 }  // namespace pn
@@ -653,7 +692,7 @@ extern "C" int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, c
     if (c.workspace > 0) {
         A.number = call_number();
         A.arrivals = (unsigned long long *)workspace;
-        A.parts = A.arrivals + ((M + 63) / 64) * ((N + 63) / 64) * kLine;
+        A.parts = A.arrivals + ((M + c.size - 1) / c.size) * ((N + c.size - 1) / c.size) * kLine;
     }
     hipStream_t s = (hipStream_t)stream;
     return type == PN_F32    ? run_gemm<PN_F32>(A, c, s)
