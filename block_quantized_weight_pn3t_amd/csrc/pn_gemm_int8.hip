@@ -46,11 +46,15 @@ struct GemmArgs {
 // 16 bytes that stand for K past its end.
 __device__ const i32x4_t kZeros[1] = {{0, 0, 0, 0}};
 
-// 16 bytes a lane from memory to LDS, a wave's in a row from lds on. In assembly, since the compiler would have
-// every read of LDS wait for every such load.
+// 16 bytes a lane from memory to LDS, a wave's in a row from lds on (ONCE: of lines that are read once). In assembly,
+// since the compiler would have every read of LDS wait for every such load.
+template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(const int8_t *p, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(p) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 
 // An offset that is worked out where it is used, and not kept in a register for the whole loop.
@@ -96,7 +100,7 @@ struct Stream {
     static constexpr int BYTES = WAVES * STAGES * STAGE + 2 * SUMS + (MOST + 32) * 4;
 };
 
-template <int T, int EIGHTS>
+template <int T, int EIGHTS, bool ONCE>
 __global__ void __launch_bounds__(256) gemm_int8_stream_kernel(GemmArgs A)
 {
     typedef Stream<EIGHTS> S;
@@ -127,8 +131,8 @@ __global__ void __launch_bounds__(256) gemm_int8_stream_kernel(GemmArgs A)
         const uint32_t to = stages + next_stage * S::STAGE;
 #pragma unroll
         for (int j = 0; j < S::ROWS / 8; j++)
-            load_lds(in ? A.w + (n0 + min(next_row + 8 * j + r, rows - 1)) * A.K + k : reinterpret_cast<const int8_t *>(kZeros),
-                     to + j * 1024);
+            load_lds<ONCE>(in ? A.w + (n0 + min(next_row + 8 * j + r, rows - 1)) * A.K + k : reinterpret_cast<const int8_t *>(kZeros),
+                           to + j * 1024);
 #pragma unroll
         for (int j = 0; j < EIGHTS; j++)
             load_lds(in ? A.a + min(8 * j + r, (int)A.M - 1) * A.K + k : reinterpret_cast<const int8_t *>(kZeros),
@@ -619,16 +623,23 @@ static int launch_gemm(const GemmArgs &A, unsigned blocks, int threads, int byte
     return launch_status();
 }
 
+template <int T, bool ONCE>
+static int run_stream(const GemmArgs &A, unsigned blocks, hipStream_t s)
+{
+    return A.M <= 8    ? launch_gemm<gemm_int8_stream_kernel<T, 1, ONCE>>(A, blocks, 256, Stream<1>::BYTES, s)
+           : A.M <= 16 ? launch_gemm<gemm_int8_stream_kernel<T, 2, ONCE>>(A, blocks, 256, Stream<2>::BYTES, s)
+                       : launch_gemm<gemm_int8_stream_kernel<T, 4, ONCE>>(A, blocks, 256, Stream<4>::BYTES, s);
+}
+
 template <int T>
 static int run_gemm(GemmArgs A, const GemmCut &c, hipStream_t s)
 {
     if (c.size == 0) {
-        // one workgroup a CU, as many rows each as it takes
+        // One workgroup a CU, as many rows each as it takes. Weights that the memory's cache (256 MB) cannot keep beside
+        // others until their next use pass it by: 178 MB 32.8 us, 35.3 through it; 89 MB, partly kept, 16.4 and 19.2 past.
         const int64_t cus = device_cus();
         const unsigned blocks = (unsigned)std::max(std::min((A.N + 7) / 8, cus), (A.N + 1023) / 1024);
-        return A.M <= 8    ? launch_gemm<gemm_int8_stream_kernel<T, 1>>(A, blocks, 256, Stream<1>::BYTES, s)
-               : A.M <= 16 ? launch_gemm<gemm_int8_stream_kernel<T, 2>>(A, blocks, 256, Stream<2>::BYTES, s)
-                           : launch_gemm<gemm_int8_stream_kernel<T, 4>>(A, blocks, 256, Stream<4>::BYTES, s);
+        return A.N * A.K >= (int64_t)128 << 20 ? run_stream<T, true>(A, blocks, s) : run_stream<T, false>(A, blocks, s);
     }
     A.tiles_m = (int)((A.M + c.size - 1) / c.size);
     A.tiles_n = (int)((A.N + c.size - 1) / c.size);

@@ -12,7 +12,7 @@
 // after the first batches is rare (about top / n of the logits at the n-th); then each lane offers its
 // best, and few are put in one by one, many are sorted among the lanes and merged.
 //
-// Memory bound for long rows: 2047 of 248,320 bf16 204 us with the five likeliest (5.0 TB/s; a copy reaches 4.9, the
+// Memory bound for long rows: 2047 of 248,320 bf16 190 us with the five likeliest (5.4 TB/s; a copy reaches 4.9, the
 // exponentials and the rest would take about 150 by themselves). One row of fp32 15.6 us with 20, 10.1 with none, of
 // which a launch and a first load are 5. A wave reads batches of 4 KB, one ahead; a row is shared by up to 64
 // workgroups where there are few, and the last to arrive joins them (pn_arrive.h).
@@ -190,7 +190,8 @@ struct Batch {
         for (int i = 0; i < LOADS; i++) {
             const int at = base + i * 64 * VEC;
             if (at + 64 * VEC <= V) {
-                v[i] = *reinterpret_cast<const EV *>(row + at + lane * VEC);
+                // each line is read once (2047 rows of 248,320 bf16: 190 us, 204 by ordinary loads)
+                v[i] = __builtin_nontemporal_load(reinterpret_cast<const EV *>(row + at + lane * VEC));
             } else {
 #pragma unroll
                 for (int j = 0; j < VEC; j++)
