@@ -11,15 +11,21 @@
 //   cache    32 tokens of one KV head, dealt to the lanes as pn_cache_write deals them. A key's lane holds
 //            four channels and loads its partner's four beside them (the same cache lines, so no more
 //            memory traffic).
-//   queries  a thread has a token, both halves of four pairs (or four channels that stay) and up to kTurn
+//   queries  a thread has a token, both halves of four or eight pairs (or as many channels that stay) and some
 //            heads, so cosines and sines are loaded once for all of them and queries once.
+//
+// Measured: 16,384 tokens of 24 and 4 heads of 256, bf16, all channels turned 111 us (4.7 TB/s; a copy reaches
+// 4.9); 8192 of them in fp32, a quarter turned, 98 us (5.0); with four heads a thread and eight channels 134 us, too
+// few waves; with channels that stay in a branch of their own 79 us for 52 of bf16, a quarter turned; queries
+// kept in the caches as they are written, 3 % more.
 #include <algorithm>
 
 #include "pn_cache_put.h"
 
 namespace pn {
 
-constexpr int kTurn = 4;  // heads a thread of the queries' workgroups turns
+// Heads a thread of the queries' workgroups turns, with `channels` a unit (as many as leave room for four waves a SIMD).
+__host__ __device__ constexpr int turn_heads(int channels, bool pairs) { return channels == 8 && !pairs ? 2 : 4; }
 
 struct AppendArgs {
     Plain k, v, q;
@@ -29,7 +35,7 @@ struct AppendArgs {
     const int64_t *positions, *slots;
     int64_t rows, T;
     int rot, Hq, cache_blocks;  // workgroups of the first kind, before the others
-    int units;         // of a token and head: four pairs or four channels each
+    int units;         // of a token and head
     int units_mul;     // n / units = n * units_mul >> 16 for n < 256
     int tokens_a_block, head_blocks;
 };
@@ -57,19 +63,59 @@ __device__ __forceinline__ f32x4_t turn_pairs(f32x4_t x, f32x2_t c, f32x2_t s)
                    turn_a(x[2], x[3], c[1], s[1]), turn_b(x[2], x[3], c[1], s[1])};
 }
 
-template <int T, bool VEC>
-__device__ __forceinline__ void put4(void *base, int64_t at, f32x4_t x)
+// CH channels of a query: 16 bytes where they are aligned (VEC), one by one elsewhere. What goes out is read by the
+// next kernel at the earliest, so it is not kept in the caches that the rest passes through.
+template <int T, int CH, bool VEC>
+__device__ __forceinline__ void get(const void *base, int64_t at, float (&x)[CH])
 {
     typedef typename Elem<T>::type E;
-    typedef E E4 __attribute__((ext_vector_type(4)));
-    E *const p = reinterpret_cast<E *>(base) + at;
+    typedef E EV __attribute__((ext_vector_type(CH)));
+    const E *const p = reinterpret_cast<const E *>(base) + at;
     if constexpr (VEC) {
-        *reinterpret_cast<E4 *>(p) = E4{(E)x[0], (E)x[1], (E)x[2], (E)x[3]};
+        const EV v = *reinterpret_cast<const EV *>(p);
+#pragma unroll
+        for (int j = 0; j < CH; j++)
+            x[j] = (float)v[j];
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+        for (int j = 0; j < CH; j++)
+            x[j] = (float)p[j];
+    }
+}
+template <int T, int CH, bool VEC>
+__device__ __forceinline__ void put(void *base, int64_t at, const float (&x)[CH])
+{
+    typedef typename Elem<T>::type E;
+    typedef E EV __attribute__((ext_vector_type(CH)));
+    E *const p = reinterpret_cast<E *>(base) + at;
+    if constexpr (VEC) {
+        EV v;
+#pragma unroll
+        for (int j = 0; j < CH; j++)
+            v[j] = (E)x[j];
+        __builtin_nontemporal_store(v, reinterpret_cast<EV *>(p));
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; j++)
             p[j] = (E)x[j];
     }
+}
+// CH cosines or sines.
+template <int CH>
+__device__ __forceinline__ void get_angles(const float *p, float (&x)[CH])
+{
+#pragma unroll
+    for (int i = 0; i < CH; i += CH % 4 ? 2 : 4)
+        if constexpr (CH % 4) {
+            const f32x2_t v = *reinterpret_cast<const f32x2_t *>(p + i);
+            x[i] = v[0];
+            x[i + 1] = v[1];
+        } else {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(p + i);
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                x[i + j] = v[j];
+        }
 }
 
 // Keys and values of 32 tokens of a KV head.
@@ -130,10 +176,11 @@ __device__ __forceinline__ void append_cache(const CacheView &c, const AppendArg
     }
 }
 
-// Queries of some tokens and kTurn heads.
-template <int T, bool VEC, bool PAIRS>
+// Queries of some tokens and kTurn heads, CH channels a unit.
+template <int T, int CH, bool VEC, bool PAIRS>
 __device__ __forceinline__ void turn_queries(const AppendArgs &A, uint32_t block)
 {
+    constexpr int kTurn = turn_heads(CH, PAIRS);
     const uint32_t run = block / (uint32_t)A.head_blocks;
     const int h0 = (int)(block - run * (uint32_t)A.head_blocks) * kTurn;
     const int n = ((int)threadIdx.x * A.units_mul) >> 16;
@@ -143,82 +190,102 @@ __device__ __forceinline__ void turn_queries(const AppendArgs &A, uint32_t block
         return;
     const int heads = min(kTurn, A.Hq - h0), half = A.rot / 2;
     const int64_t from = token * A.q.token + h0 * A.q.head, to = token * A.q_out_token + h0 * A.q_out_head;
-    const int turned = A.rot / (PAIRS ? 4 : 8);  // units that turn
-    if (u >= turned || PAIRS) {
-        // four channels: they stay, or are two pairs
-        const int ch = PAIRS ? 4 * u : A.rot + 4 * (u - turned);
-        f32x4_t x[kTurn];
+    const int turned = A.rot / (PAIRS ? CH : 2 * CH);  // units that turn
+    const bool turns = u < turned;
+    if constexpr (PAIRS) {
+        // CH channels: pairs of neighbours, or they stay
+        const int ch = CH * u;
+        float x[kTurn][CH];
 #pragma unroll
         for (int i = 0; i < kTurn; i++)
             if (i < heads)
-                x[i] = load4<T, VEC>(A.q.p, from + i * A.q.head + ch);
-        if (PAIRS && u < turned) {
-            const float *const row = table_row(A, token);
-            const f32x2_t c = *reinterpret_cast<const f32x2_t *>(row + ch / 2);
-            const f32x2_t s = *reinterpret_cast<const f32x2_t *>(row + half + ch / 2);
+                get<T, CH, VEC>(A.q.p, from + i * A.q.head + ch, x[i]);
+        if (turns) {
+            const float *const row = table_row(A, token) + ch / 2;
+            float c[CH / 2], s[CH / 2];
+            get_angles<CH / 2>(row, c);
+            get_angles<CH / 2>(row + half, s);
 #pragma unroll
             for (int i = 0; i < kTurn; i++)
-                x[i] = turn_pairs(x[i], c, s);
+                if (i < heads)
+#pragma unroll
+                    for (int j = 0; j < CH / 2; j++) {
+                        const float a = x[i][2 * j], b = x[i][2 * j + 1];
+                        x[i][2 * j] = turn_a(a, b, c[j], s[j]);
+                        x[i][2 * j + 1] = turn_b(a, b, c[j], s[j]);
+                    }
         }
 #pragma unroll
         for (int i = 0; i < kTurn; i++)
             if (i < heads)
-                put4<T, VEC>(A.q_out, to + i * A.q_out_head + ch, x[i]);
-        return;
-    }
-    const int ch = 4 * u;
-    f32x4_t a[kTurn], b[kTurn];
+                put<T, CH, VEC>(A.q_out, to + i * A.q_out_head + ch, x[i]);
+    } else {
+        // twice CH channels: both halves of pairs, or neighbours that stay
+        const int ch = turns ? CH * u : A.rot + 2 * CH * (u - turned), other = ch + (turns ? half : CH);
+        float a[kTurn][CH], b[kTurn][CH];
 #pragma unroll
-    for (int i = 0; i < kTurn; i++)
-        if (i < heads) {
-            a[i] = load4<T, VEC>(A.q.p, from + i * A.q.head + ch);
-            b[i] = load4<T, VEC>(A.q.p, from + i * A.q.head + ch + half);
-        }
-    const float *const row = table_row(A, token);
-    const f32x4_t c = *reinterpret_cast<const f32x4_t *>(row + ch);
-    const f32x4_t s = *reinterpret_cast<const f32x4_t *>(row + half + ch);
-#pragma unroll
-    for (int i = 0; i < kTurn; i++)
-        if (i < heads) {
-            f32x4_t x, y;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                x[e] = turn_a(a[i][e], b[i][e], c[e], s[e]);
-                y[e] = turn_b(a[i][e], b[i][e], c[e], s[e]);
+        for (int i = 0; i < kTurn; i++)
+            if (i < heads) {
+                get<T, CH, VEC>(A.q.p, from + i * A.q.head + ch, a[i]);
+                get<T, CH, VEC>(A.q.p, from + i * A.q.head + other, b[i]);
             }
-            put4<T, VEC>(A.q_out, to + i * A.q_out_head + ch, x);
-            put4<T, VEC>(A.q_out, to + i * A.q_out_head + ch + half, y);
+        if (turns) {
+            const float *const row = table_row(A, token) + ch;
+            float c[CH], s[CH];
+            get_angles<CH>(row, c);
+            get_angles<CH>(row + half, s);
+#pragma unroll
+            for (int i = 0; i < kTurn; i++)
+                if (i < heads)
+#pragma unroll
+                    for (int e = 0; e < CH; e++) {
+                        const float x = a[i][e], y = b[i][e];
+                        a[i][e] = turn_a(x, y, c[e], s[e]);
+                        b[i][e] = turn_b(x, y, c[e], s[e]);
+                    }
         }
+#pragma unroll
+        for (int i = 0; i < kTurn; i++)
+            if (i < heads) {
+                put<T, CH, VEC>(A.q_out, to + i * A.q_out_head + ch, a[i]);
+                put<T, CH, VEC>(A.q_out, to + i * A.q_out_head + other, b[i]);
+            }
+    }
 }
 
-template <int FMT, int D, int T, bool VEC, bool PAIRS>
+// CH: channels of a query's unit, VEC of q and q_out (and, with fewer channels, of k and v) aligned to it.
+template <int FMT, int D, int T, int CH, bool VEC, bool PAIRS>
 __global__ void __launch_bounds__(256) append_kernel(CacheView c, AppendArgs A)
 {
     if (blockIdx.x < (uint32_t)A.cache_blocks)
         append_cache<FMT, D, T, VEC, PAIRS>(c, A, blockIdx.x);
     else
-        turn_queries<T, VEC, PAIRS>(A, blockIdx.x - (uint32_t)A.cache_blocks);
+        turn_queries<T, CH, VEC, PAIRS>(A, blockIdx.x - (uint32_t)A.cache_blocks);
 }
 
 struct AppendCall {
     CacheView c;
     AppendArgs A;
+    int channels;  // of a query's unit: 8 or 4
     bool vec, pairs;
     uint32_t blocks;
     hipStream_t s;
-    template <int FMT, int D, int T, bool VEC, bool PAIRS>
-    void launch()
+    template <int FMT, int D, int T, int CH, bool VEC>
+    int launch()
     {
-        hipLaunchKernelGGL((append_kernel<FMT, D, T, VEC, PAIRS>), dim3(blocks), dim3(256), 0, s, c, A);
+        if (pairs)
+            hipLaunchKernelGGL((append_kernel<FMT, D, T, CH, VEC, true>), dim3(blocks), dim3(256), 0, s, c, A);
+        else
+            hipLaunchKernelGGL((append_kernel<FMT, D, T, CH, VEC, false>), dim3(blocks), dim3(256), 0, s, c, A);
+        return launch_status();
     }
     template <int FMT, int D, int T>
     int operator()()
     {
-        if (vec)
-            pairs ? launch<FMT, D, T, true, true>() : launch<FMT, D, T, true, false>();
-        else
-            pairs ? launch<FMT, D, T, false, true>() : launch<FMT, D, T, false, false>();
-        return launch_status();
+        if constexpr (T != PN_F32)
+            if (channels == 8)
+                return launch<FMT, D, T, 8, true>();
+        return vec ? launch<FMT, D, T, 4, true>() : launch<FMT, D, T, 4, false>();
     }
 };
 
@@ -260,31 +327,37 @@ extern "C" int pn_cache_append(const pn_cache *cache, const pn_append_args *a, v
     int64_t blocks = (a->T + kQuads * 4 - 1) / (kQuads * 4) * c.heads;
     A.cache_blocks = (int)blocks;
     bool vec = aligned(a->k, 4 * size) && aligned(a->v, 4 * size);
+    int channels = 4;
     if (a->q) {
         A.q = Plain{a->q, a->q_token_stride, a->q_head_stride};
         A.q_out = a->q_out;
         A.q_out_token = a->q_out_token_stride;
         A.q_out_head = a->q_out_head_stride;
         A.Hq = a->Hq;
+        strides |= A.q.token | A.q.head | A.q_out_token | A.q_out_head;
+        vec = vec && aligned(a->q, 4 * size) && aligned(a->q_out, 4 * size) && (strides & 3) == 0;
+        // eight channels of 16 bits are a load of 16 bytes
+        if (size == 2 && vec && aligned(a->q, 16) && aligned(a->q_out, 16) &&
+            ((A.q.token | A.q.head | A.q_out_token | A.q_out_head) & 7) == 0 && a->rot % (a->interleaved ? 8 : 16) == 0)
+            channels = 8;
         // channels that stay are left alone where the queries are turned in place
         const bool in_place = a->q == a->q_out && a->q_token_stride == a->q_out_token_stride &&
                               a->q_head_stride == a->q_out_head_stride;
-        A.units = a->rot / (a->interleaved ? 4 : 8) + (in_place ? 0 : (cache->dim - a->rot) / 4);
+        A.units = (in_place ? a->rot : cache->dim) / (a->interleaved ? channels : 2 * channels);
         A.units_mul = (65536 + A.units - 1) / A.units;
         A.tokens_a_block = 256 / A.units;
-        A.head_blocks = (A.Hq + kTurn - 1) / kTurn;
+        const int turn = turn_heads(channels, a->interleaved);
+        A.head_blocks = (A.Hq - 1) / turn + 1;
         const int64_t runs = (a->T + A.tokens_a_block - 1) / A.tokens_a_block;
         if (runs > INT32_MAX / A.head_blocks)
             return PN_ERR_SHAPE;
         blocks += runs * A.head_blocks;
-        strides |= A.q.token | A.q.head | A.q_out_token | A.q_out_head;
-        vec = vec && aligned(a->q, 4 * size) && aligned(a->q_out, 4 * size);
     }
     if (blocks > INT32_MAX)
         return PN_ERR_SHAPE;
     if ((st = check_device()) != PN_OK)
         return st;
     return by_kind(cache->format, cache->dim, a->type,
-                   AppendCall{c, A, vec && (strides & 3) == 0, a->interleaved != 0, (uint32_t)blocks,
+                   AppendCall{c, A, channels, vec && (strides & 3) == 0, a->interleaved != 0, (uint32_t)blocks,
                               (hipStream_t)stream});
 }
