@@ -93,7 +93,7 @@ template <int EIGHTS>
 struct Stream {
     static constexpr int WAVES = 4, ROWS = 32, TILES = (EIGHTS + 1) / 2;  // 16 tokens a tile
     static constexpr int STAGE = (ROWS + 8 * EIGHTS) * 128, LOADS = STAGE / 1024;
-    static constexpr int STAGES = EIGHTS == 4 ? 3 : 5;
+    static constexpr int STAGES = EIGHTS == 4 ? 3 : EIGHTS == 2 ? 5 : 4;
     static constexpr int ROW = ROWS + 4;                         // a token's sums in LDS, padded
     static constexpr int SUMS = WAVES * TILES * 16 * ROW * 4;    // bytes; twice, for every other tile
     static constexpr int MOST = 1024;                            // rows a workgroup has
