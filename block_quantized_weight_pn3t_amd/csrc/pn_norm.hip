@@ -12,6 +12,9 @@
 // there, and only where a quotient lies that near to a border between two codes (one number in ten thousand) is it
 // worked out in 64 bits. T has to be exact for that: a product of two 16-bit numbers is in fp32, one with an fp32
 // number is taken in 64 bits. Squares are summed in 64 bits.
+//
+// Measured: 8192 rows of 5120 bf16 with their residual to 8-bit rows 62 us (4.8 TB/s; a copy reaches 4.9), all of it in 64
+// bits 99; 4095 of 17408 bf16 to 8-bit rows 45 us (4.8); four of 5120 fp32 4.1 us.
 #include <float.h>
 
 #include "pn_cache.h"

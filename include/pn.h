@@ -408,11 +408,11 @@ int pn_add_norm(const pn_add_norm_args *a, void *stream);
  * (codes from -128 on), out of `type` (PN_F32, PN_BF16, PN_F16). The sum is exact; it is converted to
  * fp32, multiplied by a_scales[m], then by w_scales[n] in fp32 and rounded to its type: three
  * roundings of 2^-24 and the type's. K a positive multiple of 16, at most PN_GEMM_INT8_MAX_K (sums
- * stay below 2^31; else PN_ERR_SHAPE); M and N any. a and w 16-byte aligned.
+ * stay below 2^31; else PN_ERR_SHAPE); M and N below 2^31. a and w 16-byte aligned.
  * Deterministic. workspace: pn_gemm_int8_workspace_bytes of device memory (16-byte aligned), with any
  * content to begin with, overwritten; calls that may overlap need one each. */
 #define PN_GEMM_INT8_MAX_K 131056
-int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K); /* 0 where none is needed */
 
 int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t *w,
                  const float *w_scales, int64_t N, int64_t K, int type, void *out,
