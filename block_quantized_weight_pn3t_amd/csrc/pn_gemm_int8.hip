@@ -47,7 +47,8 @@ struct GemmArgs {
 __device__ const i32x4_t kZeros[1] = {{0, 0, 0, 0}};
 
 // 16 bytes a lane from memory to LDS, a wave's in a row from lds on (ONCE: of lines that are read once). In assembly,
-// since the compiler would have every read of LDS wait for every such load.
+// since the compiler would have every read of LDS wait for every such load. (m0 is a reserved register: the compiler keeps
+// nothing in it from one statement to another.)
 template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(const int8_t *p, uint32_t lds)
 {
