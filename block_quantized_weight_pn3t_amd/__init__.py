@@ -630,13 +630,15 @@ def _rows(t, name, dtype, shape, dev, written=False):
     return row
 
 
-def _plain_kind(t, name, dim, dev, T):
-    """The element type id of a plain tensor of `dim` dimensions."""
+def _plain(t, name, dim, dev, T):
+    """The element type id and strides of a plain tensor of `dim` dimensions, the last of them contiguous."""
     kind = T.kinds.get(t.dtype)
-    if kind is None or t.dim() != dim or t.get_device() != dev:
-        raise ValueError(f"{name} must be a tensor of {dim} dimensions of float32, bfloat16 or float16 on the current "
-                         f"device ({dev}), got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return kind
+    strides = t.stride()
+    if kind is None or len(strides) != dim or t.get_device() != dev or (strides[-1] != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be a tensor of {dim} dimensions, the last contiguous, of float32, bfloat16 or "
+                         f"float16 on the current device ({dev}), got {t.dtype} {tuple(t.shape)} with strides {strides} "
+                         f"on {t.device}")
+    return kind, strides
 
 
 def _workspace(t, dev, T):
@@ -652,9 +654,8 @@ def int8_quantize_rows(x, codes, scales, stream=None):
     (pn_int8_quantize_rows): activations before gemm_int8, and its weights."""
     T = _names()
     dev = T.device()
-    kind = _plain_kind(x, "x", 2, dev, T)
+    kind, (row, _) = _plain(x, "x", 2, dev, T)
     shape = n, k = x.shape
-    row = _rows(x, "x", x.dtype, shape, dev)
     codes_at, scales_at = _flat(codes, "codes", T.i8, shape, dev), _flat(scales, "scales", T.f32, (n,), dev)
     _check(_lib.pn_int8_quantize_rows(kind, x.data_ptr(), row, n, k, codes_at, scales_at, _handle(stream, T)),
            "pn_int8_quantize_rows")
@@ -669,11 +670,12 @@ def add_norm(x, weight, eps, out=None, codes=None, scales=None, residual=None, s
     sum [N, K] <- x + residual, which the norm is of; sum and out may be x or residual themselves."""
     T = _names()
     dev = T.device()
-    kind = _plain_kind(x, "x", 2, dev, T)
+    kind, (x_row, _) = _plain(x, "x", 2, dev, T)
     shape = n, k = x.shape
     dt = x.dtype
-    x_row = _rows(x, "x", dt, shape, dev)
-    weight_kind = _plain_kind(weight, "weight", 1, dev, T)
+    weight_kind = T.kinds.get(weight.dtype)
+    if weight_kind is None:
+        _misfit(weight, "weight", "a floating type", (k,), dev, "a contiguous tensor")
     weight_at = _flat(weight, "weight", weight.dtype, (k,), dev)
     residual_at = residual_row = sum_at = sum_row = out_at = out_row = codes_at = scales_at = 0
     if residual is not None:
@@ -704,7 +706,7 @@ def gemm_int8(a, a_scales, w, w_scales, out, workspace=None, stream=None):
     tensor of gemm_int8_workspace_bytes."""
     T = _names()
     dev = T.device()
-    kind = _plain_kind(out, "out", 2, dev, T)
+    kind, _ = _plain(out, "out", 2, dev, T)
     if a.dim() != 2 or w.dim() != 2:
         raise ValueError(f"a and w must be [M, K] and [N, K], got {tuple(a.shape)} and {tuple(w.shape)}")
     m, k = a.shape
@@ -737,10 +739,11 @@ def cache_append(cache, k, v, slots, rotation, positions=None, q=None, q_out=Non
     its own number unless given. interleaved: channels (2j, 2j + 1) turn together, not (j, j + rot / 2)."""
     T = _names()
     dev = T.device()
-    kind = _plain_kind(k, "k", 3, dev, T)
+    kind, (k_token, k_head, _) = _plain(k, "k", 3, dev, T)
     n, dt = k.shape[0], k.dtype
     shape = (n, cache.heads, cache.dim)
-    k_token, k_head = _heads(k, "k", dt, shape, dev)
+    if k.shape != shape:
+        _misfit(k, "k", dt, shape, dev, "a tensor")
     v_token, v_head = _heads(v, "v", dt, shape, dev)
     slots_at = _flat(slots, "slots", T.i64, (n,), dev)
     if rotation.dim() != 2:
@@ -780,9 +783,8 @@ def logprobs(logits, tokens=None, logprob=None, workspace=None, rank=None, entro
     tokens: those of them that are given. workspace: a uint8 tensor of logprobs_workspace_bytes."""
     T = _names()
     dev = T.device()
-    kind = _plain_kind(logits, "logits", 2, dev, T)
-    R, V = shape = logits.shape
-    row = _rows(logits, "logits", logits.dtype, shape, dev)
+    kind, (row, _) = _plain(logits, "logits", 2, dev, T)
+    R, V = logits.shape
     one = (R,)
     tokens_at = logprob_at = rank_at = entropy_at = lse_at = ids_at = top_at = top = 0
     if tokens is not None:

@@ -239,11 +239,13 @@ __device__ __forceinline__ void take(const float (&x)[Batch<T>::PER], float m, i
             const bool in = left != 0 && key > lane_key(list, top - 1);
             left = in ? left & ~(1u << at) : 0;
             u64 offers = __ballot(in);
-            if (__popcll(offers) > 8)
-                list = merged(list, sorted(in ? key : 0, lane), lane);
-            else
+            if (__popcll(offers) > 8) {
+                const u64 fresh = sorted(in ? key : 0, lane);
+                list = lane_key(list, 0) ? merged(list, fresh, lane) : fresh;
+            } else {
                 for (; offers; offers &= offers - 1)
                     list = inserted(list, lane_key(key, __ffsll(offers) - 1), lane);
+            }
         }
     }
     const u64 last = lane_key(list, top - 1);
@@ -274,10 +276,14 @@ __device__ __forceinline__ void write_row(const LogArgs &A, int64_t row, Sums a,
     }
 }
 
-// The lists of a workgroup's waves into the first one's, by twos.
+// The lists of a workgroup's waves into the first one's, by twos, behind one barrier at least.
 template <int WAVES>
-__device__ __forceinline__ u64 over_waves(u64 list, u64 (&lds)[WAVES][64], int wave, int lane)
+__device__ __forceinline__ u64 over_waves(u64 list, u64 (&lds)[WAVES][64], int wave, int lane, int top)
 {
+    if (top == 0) {
+        __syncthreads();
+        return 0;
+    }
 #pragma unroll
     for (int n = WAVES / 2; n > 0; n /= 2) {
         if (wave >= n && wave < 2 * n)
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
     // the workgroup's waves into the first
     if (lane == 0)
         lds_sums[wave] = a;
-    list = over_waves<WAVES>(list, lds_list[0], wave, lane);  // (with a barrier)
+    list = over_waves<WAVES>(list, lds_list[0], wave, lane, A.top);
     if (wave == 0) {
         a = lane < WAVES ? lds_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f, 0};
         a = over_lanes(a, A.exp2_scale);
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
 #pragma unroll
             for (int i = 0; i < n; i++)
                 in[i] = merged(in[i], in[i + n], lane);
-    list = over_waves<WAVES>(in[0], lds_list[1], wave, lane);
+    list = over_waves<WAVES>(in[0], lds_list[1], wave, lane, A.top);
     if (wave == 0)
         write_row(A, row, over_lanes(a, A.exp2_scale), list, lane, token_logit, has_token);
 }
@@ -418,9 +424,10 @@ static int log_batches(int type, int64_t V)
 }
 
 // Waves of a workgroup and workgroups of a row. Few rows: large workgroups, as many as fill the machine, since
-// arrivals at a row's word come one after another and a wave's list is joined sooner in LDS (one row: 15.6 us, 17.8 by
-// 61 workgroups of four waves). Many rows: small ones, half the machine at least; each share of a row begins its list
-// anew, which costs about as long as 30,000 of its logits (1023 rows of 248,320 fp32, top 64: 199 us whole, 217 in two).
+// arrivals at a row's word come one after another and a wave's list is joined sooner in LDS (16 rows of 248,320 fp32:
+// 17.0 us, 21.8 by 61 workgroups of four waves; one row 15.3 both ways). Many rows: small ones, half the machine at
+// least; each share of a row begins its list anew, which costs about as long as 30,000 of its logits (1023 rows of
+// 248,320 fp32, top 64: 199 us whole, 217 in two).
 static int log_waves(int64_t R) { return R < 256 ? 16 : 4; }
 static int log_groups(int64_t R, int batches)
 {
@@ -453,8 +460,9 @@ extern "C" int64_t pn_logprobs_workspace_bytes(int64_t R, int64_t V, int top)
 {
     if (!logits_fit(R, V, top) || R == 0)
         return 0;
-    // of the type that has more batches, and the same whether a row is shared or not
-    return R * kLine * 8 + R * log_groups(R, log_batches(PN_F32, V)) * (2 + top) * 8;
+    // as many shares of rows as log_groups deals at most, of the type that has more batches: enough for fewer rows too
+    const int64_t shares = std::min(R * std::min(64, (log_batches(PN_F32, V) + 3) / 4), R + 511);
+    return R * kLine * 8 + shares * (2 + top) * 8;
 }
 
 extern "C" int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t workspace_bytes, void *stream)

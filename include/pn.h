@@ -410,7 +410,8 @@ int pn_add_norm(const pn_add_norm_args *a, void *stream);
  * roundings of 2^-24 and the type's. K a positive multiple of 16, at most PN_GEMM_INT8_MAX_K (sums
  * stay below 2^31; else PN_ERR_SHAPE); M and N below 2^31. a and w 16-byte aligned.
  * Deterministic. workspace: pn_gemm_int8_workspace_bytes of device memory (16-byte aligned), with any
- * content to begin with, overwritten; calls that may overlap need one each. */
+ * content to begin with, overwritten; calls that may overlap need one each. Fewer rows can need more
+ * of it: for calls of several sizes take the largest. */
 #define PN_GEMM_INT8_MAX_K 131056
 int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K); /* 0 where none is needed */
 
@@ -465,7 +466,8 @@ int pn_cache_append(const pn_cache *cache, const pn_append_args *a, void *stream
  * Maxima, exponentials and sums in fp32 relative to a row's running maximum. Deterministic.
  * 1 <= V < 2^30, 0 <= top <= PN_LOGPROBS_MAX_TOP, scale positive and finite (else PN_ERR_SHAPE).
  * workspace: pn_logprobs_workspace_bytes of device memory (16-byte aligned), with any content to
- * begin with, overwritten; calls that may overlap need one each. */
+ * begin with, overwritten; calls that may overlap need one each. Enough for fewer rows, a smaller V
+ * or top too. */
 #define PN_LOGPROBS_MAX_TOP 64
 typedef struct pn_logprobs_args {
     int type;               /* of the logits: PN_F32, PN_BF16 or PN_F16 */

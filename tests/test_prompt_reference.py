@@ -150,6 +150,16 @@ def test_logprobs_refusals(kw, status):
     assert logp(**kw) == status
 
 
+def test_logprobs_workspace_is_enough_for_less():
+    for V in (1, 2048, 9000, 248320):
+        for top in (0, 20):
+            need = [pn.logprobs_workspace_bytes(R, V, top) for R in range(1, 1100)]
+            assert need == sorted(need)
+    for R in (1, 3, 255, 256, 511, 600):
+        need = [pn.logprobs_workspace_bytes(R, V, 20) for V in range(1, 300000, 997)]
+        assert need == sorted(need)
+
+
 def test_logprobs_workspace():
     assert L.pn_logprobs(None, fake, 0, None) == -4
     for R, V, top in ((-1, 10, 0), (1, 0, 0), (1, 1 << 30, 0), (1, 10, 65), (1, 10, -1), (0, 10, 0)):
