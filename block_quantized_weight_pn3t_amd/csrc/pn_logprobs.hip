@@ -12,8 +12,8 @@
 // after the first batches is rare (about top / n of the logits at the n-th); then each lane offers its
 // best, and few are put in one by one, many are sorted among the lanes and merged.
 //
-// Memory bound for long rows: 2047 of 248,320 bf16 190 us with the five likeliest (5.4 TB/s; a copy reaches 4.9, the
-// exponentials and the rest would take about 150 by themselves). One row of fp32 15.6 us with 20, 10.1 with none, of
+// Memory bound for long rows: 2047 of 248,320 bf16 188 us with the five likeliest (5.4 TB/s; a copy reaches 4.9, the
+// exponentials and the rest would take about 150 by themselves). One row of fp32 13.2 us with 20, 8.3 with none, of
 // which a launch and a first load are 5. A wave reads batches of 4 KB, one ahead; a row is shared by up to 64
 // workgroups where there are few, and the last to arrive joins them (pn_arrive.h).
 #include <float.h>
@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
 {
     typedef Batch<T> B;
     typedef typename B::E E;
+    constexpr bool SHARED = WAVES < 16;  // whether rows can have several workgroups (log_groups)
     __shared__ Sums lds_sums[WAVES];
-    __shared__ u64 lds_list[2][WAVES][64];
+    __shared__ u64 lds_list[1 + SHARED][WAVES][64];
     __shared__ bool last;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = blockIdx.x / (unsigned)A.groups;
@@ -370,10 +371,10 @@ __global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
     if (wave == 0) {
         a = lane < WAVES ? lds_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f, 0};
         a = over_lanes(a, A.exp2_scale);
-        if (A.groups == 1)
+        if (!SHARED || A.groups == 1)
             write_row(A, row, a, list, lane, token_logit, has_token);
     }
-    if (A.groups == 1)
+    if (!SHARED || A.groups == 1)
         return;
     if (wave == 0) {
         const int64_t at = row * A.groups + group;
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
 #pragma unroll
             for (int i = 0; i < n; i++)
                 in[i] = merged(in[i], in[i + n], lane);
-    list = over_waves<WAVES>(in[0], lds_list[1], wave, lane, A.top);
+    list = over_waves<WAVES>(in[0], lds_list[SHARED], wave, lane, A.top);
     if (wave == 0)
         write_row(A, row, over_lanes(a, A.exp2_scale), list, lane, token_logit, has_token);
 }
@@ -423,25 +424,38 @@ static int log_batches(int type, int64_t V)
     return (int)((V + all - 1) / all);
 }
 
-// Waves of a workgroup and workgroups of a row. Few rows: large workgroups, as many as fill the machine, since
-// arrivals at a row's word come one after another and a wave's list is joined sooner in LDS (16 rows of 248,320 fp32:
-// 17.0 us, 21.8 by 61 workgroups of four waves; one row 15.3 both ways). Many rows: small ones, half the machine at
-// least; each share of a row begins its list anew, which costs about as long as 30,000 of its logits (1023 rows of
-// 248,320 fp32, top 64: 199 us whole, 217 in two).
-static int log_waves(int64_t R) { return R < 256 ? 16 : 4; }
+// Waves of a workgroup and workgroups of a row.
+// Up to 512 rows: workgroups of eight waves, which a CU holds two of, and as many a row as the machine has CUs for; more
+// begin more lists anew, and a second round of them costs the first one's time again. 195 rows of 65,536 bf16, 5
+// likeliest: 20.0 us by one a row, 23.6 by two, 33.8 by two of 16 waves; 48 rows of 248,320: 20.6 by five a row, 23.3 by
+// ten, 23.8 by five of 16 waves, 24.6 by five of four; one row of 248,320 fp32, 20 likeliest: 13.4, by 16 waves 15.6.
+// A row of nine to 16 batches: one workgroup of 16 waves, which spares the hand-over (one row of 20,000 bf16: 5.8 us, 7.4
+// by two of eight).
+// More than 512 rows: one of four waves each, which a CU holds four of (1000 rows of 65,536 bf16, 5 likeliest: 38.4 us,
+// 47.4 by eight waves; 511 rows: 27.6 by eight, 26.9 by four, 30.7 by two of four a row).
+// 257 to 341 long rows: three of four waves each, as the second workgroups of eight waves would fall to few CUs (300 rows
+// of 248,320 bf16, 5 likeliest: 48.7 us, 56.8 by eight waves; of 65,536 26.2 and 26.3, of 20,000 17.4 and 15.7).
+static int log_waves(int64_t R, int batches)
+{
+    if (R > 512 || (R > 256 && R <= 341 && batches > 64))
+        return 4;
+    return R <= 256 && batches > 8 && batches <= 16 ? 16 : 8;
+}
 static int log_groups(int64_t R, int batches)
 {
-    const int waves = log_waves(R);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (batches + waves - 1) / waves),
-                                                       ((waves == 16 ? 256 : 512) + R - 1) / R));
+    const int waves = log_waves(R, batches);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({64, (batches + waves - 1) / waves, (waves == 4 ? 1024 : 256) / R}));
 }
 
 template <int T>
 static int launch_log(const LogArgs &A, int64_t R, hipStream_t s)
 {
     const dim3 grid((unsigned)(R * A.groups));
-    if (log_waves(R) == 16)
+    const int waves = log_waves(R, A.batches);
+    if (waves == 16)
         hipLaunchKernelGGL((logprobs_kernel<T, 16>), grid, dim3(1024), 0, s, A);
+    else if (waves == 8)
+        hipLaunchKernelGGL((logprobs_kernel<T, 8>), grid, dim3(512), 0, s, A);
     else
         hipLaunchKernelGGL((logprobs_kernel<T, 4>), grid, dim3(256), 0, s, A);
     return launch_status();
@@ -461,7 +475,7 @@ extern "C" int64_t pn_logprobs_workspace_bytes(int64_t R, int64_t V, int top)
     if (!logits_fit(R, V, top) || R == 0)
         return 0;
     // as many shares of rows as log_groups deals at most, of the type that has more batches: enough for fewer rows too
-    const int64_t shares = std::min(R * std::min(64, (log_batches(PN_F32, V) + 3) / 4), R + 511);
+    const int64_t shares = std::min(R * std::min(64, (log_batches(PN_F32, V) + 3) / 4), std::max<int64_t>(R, 1024));
     return R * kLine * 8 + shares * (2 + top) * 8;
 }
 

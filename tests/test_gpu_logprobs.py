@@ -96,6 +96,16 @@ def test_rows(env, type_, R, V):
     check(env, 3 * rng.normal(size=(R, V)), type_, top=20)
 
 
+@pytest.mark.parametrize("type_", ["float32", "bfloat16"])
+@pytest.mark.parametrize("R,V", [(1, 1200007), (2, 8193), (3, 16385), (3, 32769), (128, 20001), (129, 20001), (256, 16384),
+                                 (256, 16385), (257, 9001), (257, 131073), (341, 65537), (342, 65537), (512, 8193), (513, 8193)])
+def test_rows_at_the_cuts(env, type_, R, V):
+    """Rows shared by many, two and no workgroups, of four, eight and 16 waves."""
+    rng = np.random.default_rng(R)
+    check(env, 3 * rng.normal(size=(R, V)), type_, top=5)
+    check(env, 3 * rng.normal(size=(R, V)), type_, top=0)
+
+
 @pytest.mark.parametrize("top", [0, 1, 2, 7, 8, 9, 32, 63, 64])
 @pytest.mark.parametrize("V", [5, 64, 3000, 50001])
 def test_top(env, top, V):
