@@ -35,7 +35,6 @@ struct GemmArgs {
     int K;
     void *out;
     int tiles_m, tiles_n;  // of the outputs
-    int vec;               // rows of out take stores of 16 bytes
     int splits;            // parts of K, of `each` lines
     int each;
     unsigned long long number;     // of the call (pn_arrive.h)
@@ -235,6 +234,7 @@ __global__ void __launch_bounds__(256) gemm_int8_tile_kernel(GemmArgs A)
     typedef Square<SIZE, STAGES> S;
     typedef typename Elem<T>::type E;
     typedef E E4 __attribute__((ext_vector_type(4)));
+    typedef E E4Any __attribute__((ext_vector_type(4), aligned(sizeof(E))));  // rows of out of any alignment
     extern __shared__ i32x4_t lds[];  // [stage][a, w][row][piece]
     __shared__ bool last;
     char *const base = reinterpret_cast<char *>(lds);
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(256) gemm_int8_tile_kernel(GemmArgs A)
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 v[e] = (E)((float)acc[i][j][e] * sa * sw[j][e]);
-            if (A.vec && n + 4 <= A.N) {
-                *reinterpret_cast<E4 *>(p) = v;
+            if (n + 4 <= A.N) {
+                *reinterpret_cast<E4Any *>(p) = v;
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; e++)
@@ -518,9 +518,11 @@ __global__ void __launch_bounds__(512, 2) gemm_int8_large_kernel(GemmArgs A)
     barrier();
 
     // A lane has token row of 16 and four rows of w, 4g .. 4g + 3: sixteen tokens at a time go through the wave's own
-    // part of LDS to be written as whole lines.
+    // part of LDS to be written as whole lines. (Vectors at any address: 2846 x 14445 x 1024, bf16, 64 us, 116
+    // by single numbers; 14448 wide 63.)
     constexpr int VEC = 16 / sizeof(E), LANES = 64 / VEC, STRIDE = 64 + VEC;  // lanes and elements a token's row of 64
     typedef E EV __attribute__((ext_vector_type(VEC)));
+    typedef E EVAny __attribute__((ext_vector_type(VEC), aligned(sizeof(E))));  // rows of out of any alignment
     typedef E E4 __attribute__((ext_vector_type(4)));
     E *const stage = reinterpret_cast<E *>(lds) + wave * 16 * STRIDE;
     const int64_t n_wave = n0 + wc * 64, m_wave = m0 + wr * 128;
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(512, 2) gemm_int8_large_kernel(GemmArgs A)
                 E *const p = reinterpret_cast<E *>(A.out) + (m + at) * A.out_stride + n_wave + c;
                 if (m + at >= A.M)
                     continue;
-                if (A.vec && n_wave + c + VEC <= A.N) {
-                    *reinterpret_cast<EV *>(p) = v;
+                if (n_wave + c + VEC <= A.N) {
+                    *reinterpret_cast<EVAny *>(p) = v;
                 } else {
 #pragma unroll
                     for (int e = 0; e < VEC; e++)
@@ -707,7 +709,6 @@ extern "C" int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, c
     A.out_stride = out_stride;
     A.K = (int)K;
     A.out = out;
-    A.vec = aligned(out, 16) && (out_stride * size & 15) == 0;
     if (c.workspace > 0) {
         A.number = call_number();
         A.arrivals = (unsigned long long *)workspace;
