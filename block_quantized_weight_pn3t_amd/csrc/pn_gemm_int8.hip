@@ -597,20 +597,23 @@ static GemmCut gemm_cut(int64_t M, int64_t N, int64_t K)
         return c;
     // What is estimated to be soonest, in us: rounds of workgroups, each some time a line and some to begin and end,
     // and the joining of K's parts. Measured for a line: 0.25 and 0.38 with one and two workgroups a CU (64), 0.5
-    // (128), 0.92 (256). So 64 x 1024 x 5120 is four parts in tiles of 64 (9.6 us; whole 12.3, in tiles of 128 20), 256 x
-    // 5120 x 17408 three in tiles of 128 (44; 86 whole, 59 in tiles of 64), 1024 x 5120 x 6144 tiles of 128 (57; 60 each
-    // in those of 64 and 256), 2048 x 6144 x 5120 tiles of 256 (61; 92 in those of 128).
+    // (128; half of it where a last round leaves most CUs idle), 0.92 (256). So 64 x 1024 x 5120 is four parts in tiles
+    // of 64 (9.6 us; whole 12.3, in tiles of 128 20), 256 x 5120 x 17408 three in tiles of 128 (44; 86 whole, 59 in tiles
+    // of 64), 1024 x 5120 x 5120 tiles of 128 (45; 50 in those of 256), 2048 x 6144 x 5120 tiles of 256 (61; 92 in those
+    // of 128), 4096 x 5120 x 1024 too (36; 48), 777 x 5120 x 1024 tiles of 64 (16.1; 18.6 in those of 128).
     double best = INFINITY;
     for (const int size : {64, 128, 256}) {
         const int64_t t = up(M, size) * up(N, size), slots = size == 64 ? 2 * cus : cus;
-        const double edge = size == 64 ? 1.0 : size == 128 ? 2.0 : 8.5;
+        const double edge = size == 64 ? 2.3 : size == 128 ? 5.2 : 10.0;
         for (int splits = 1; splits <= (size == 256 ? 1 : std::min<int64_t>(8, lines / 4 + 1)); splits++) {
             const int64_t each = up(lines, splits), blocks = t * splits;
             if (up(lines, each) != splits || (splits > 1 && blocks > 2 * slots))
                 continue;
             const double line = size == 64 ? (blocks <= cus ? 0.25 : 0.38) : size == 128 ? 0.5 : 0.92;
-            const double join = splits == 1 ? 0.0 : size == 64 ? 2.3 + 0.6 * splits : 2.0 + 1.45 * splits;
-            const double time = (double)up(blocks, slots) * ((double)each * line + edge) + join;
+            const double join = splits == 1 ? 0.0 : size == 64 ? 2.3 + 0.6 * splits : 1.45 * splits;
+            const int64_t idle = size == 128 && blocks > slots ? up(blocks, slots) * slots - blocks : 0;
+            const double time = (double)up(blocks, slots) * ((double)each * line + edge) + join -
+                                (double)each * 0.25 * (double)idle / (double)slots;
             if (time < best) {
                 best = time;
                 c.size = size;

@@ -74,6 +74,12 @@ def test_types(env, type_, M, N, K):
     check(env, M, N, K, type_, 3)
 
 
+@pytest.mark.parametrize("K", [16, 96, 128, 144, 256, 272, 400, 528])
+@pytest.mark.parametrize("M,N,type_", [(1030, 10245, "bfloat16"), (600, 17410, "float32"), (3001, 5123, "float16")])
+def test_many_outputs_of_few_products(env, M, N, K, type_):
+    check(env, M, N, K, type_, K)
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 130, 400])
 @pytest.mark.parametrize("type_", ["float32", "bfloat16"])
 def test_rows_of_a_wider_output(env, M, type_):
