@@ -49,7 +49,13 @@ struct Sums {
 
 __device__ __forceinline__ float greater(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
 
-// The largest and the smallest of three, NaN aside. (Left to itself the compiler quiets each operand first.)
+// From here on a maximum or minimum with a signalling NaN is the other operand, as with a quiet one. (As waves begin, with bit
+// 9 of their mode register set, IEEE, it is a NaN, which the next maximum drops, and with it what came before.) In assembly,
+// since the compiler takes the builtin for a write of memory.
+__device__ __forceinline__ void pass_nan_by() { asm volatile("s_setreg_imm32_b32 hwreg(HW_REG_MODE, 9, 1), 0"); }
+
+// The largest and the smallest of three, NaN aside after pass_nan_by(). (Left to itself the compiler quiets each operand
+// first.)
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -316,6 +322,7 @@ __global__ void __launch_bounds__(64 * WAVES, 4) logprobs_kernel(LogArgs A)
     const int token = A.tokens ? A.tokens[row] : -1;
     const bool has_token = token >= 0 && token < A.V;
     const float token_logit = has_token ? (float)x_row[token] : INFINITY;
+    pass_nan_by();
 
     Sums a{-INFINITY, 0.0f, 0.0f, 0};
     float ref = 0.0f;  // what l and t are relative to: m, or anything while they are zero
