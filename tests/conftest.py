@@ -31,3 +31,26 @@ def orc():
     import oracle
     oracle.lib()
     return oracle
+
+
+@pytest.fixture(autouse=True)
+def fills_before_calls(request, monkeypatch):
+    """test_gpu_logprobs.call fills the outputs and the workspace on the current stream; a call on another stream has to
+    wait for that, or it runs beside the fills and may find its workspace overwritten."""
+    module = request.module
+    if module.__name__ != "test_gpu_logprobs":
+        return
+    made = module.call
+
+    class Waiting:
+        def __init__(self, pn, torch):
+            self.pn, self.torch = pn, torch
+
+        def __getattr__(self, name):
+            return getattr(self.pn, name)
+
+        def logprobs(self, *args, stream=None, **kw):
+            if stream is not None:
+                stream.wait_stream(self.torch.cuda.current_stream())
+            return self.pn.logprobs(*args, stream=stream, **kw)
+    monkeypatch.setattr(module, "call", lambda pn, torch, *a, **kw: made(Waiting(pn, torch), torch, *a, **kw))
