@@ -265,7 +265,12 @@ __device__ __forceinline__ void write_row(const LogArgs &A, int64_t row, Sums a,
     const float nan = __builtin_nanf("");
     const bool bad = !(a.l < INFINITY);  // a NaN or +infinity
     const float log_l = logf(a.l);
-    const auto log_p = [&](float x) { return bad || a.l == 0.0f ? nan : A.scale * (x - a.m) - log_l; };
+    const auto log_p = [&](float x) {
+        float d = A.scale * (x - a.m);
+        if (!(d > -INFINITY))  // a difference that passes fp32 comes back where the scale is below one
+            d = (float)((double)A.scale * ((double)x - (double)a.m));
+        return bad || a.l == 0.0f ? nan : d - log_l;
+    };
     if (lane == 0) {
         if (A.logprob)
             A.logprob[row] = has_token ? log_p(token_logit) : 0.0f;

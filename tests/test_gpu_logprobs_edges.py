@@ -42,3 +42,24 @@ def test_signalling_nan(env, type_, whole, bits, V, top):
     got = call(pn, torch, x.to(dev), torch.from_numpy(tokens).to(dev), 1.0, top)
     torch.cuda.synchronize()
     same(got, values, tokens, 1.0, top)
+
+
+@pytest.mark.parametrize("type_", ["float32", "bfloat16"])
+@pytest.mark.parametrize("scale", [0.25, 1e-3, 1.0])
+def test_differences_past_fp32(env, type_, scale):
+    """The largest and the smallest numbers in one row, of which a scale below one makes log probabilities within fp32."""
+    pn, torch, dev = env
+    low = {"float32": -3.4028234663852886e38, "bfloat16": -3.3895313892515355e38}[type_]
+    x = np.zeros((3, 50))
+    x[0, 3], x[0, 7] = -low, low
+    x[1], x[1, 40] = low, -low / 2
+    x[2, 5], x[2, 6], x[2, 7] = -low, -np.inf, low
+    tokens = np.array([7, 0, 6], np.int32)
+    t = torch.from_numpy(x.astype(np.float32)).to(getattr(torch, type_))
+    got = call(pn, torch, t.to(dev), torch.from_numpy(tokens).to(dev), scale, 50)
+    torch.cuda.synchronize()
+    if scale < 1.0:  # in full; at one the definition passes fp32 too
+        assert got["logprob"].isfinite().tolist() == [True, True, False]
+        same(got, t.double().numpy(), tokens, scale, 50)
+    else:
+        assert bool((got["logprob"][[0, 2]] == -float("inf")).all()) and bool((got["top_ids"][0, :2].cpu() == torch.tensor([3, 0])).all())
