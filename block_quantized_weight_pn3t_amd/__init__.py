@@ -780,7 +780,8 @@ def logprobs(logits, tokens=None, logprob=None, workspace=None, rank=None, entro
     """Rows of logits [R, V] as distributions (pn_logprobs). logprob fp32[R] <- the log probability of
     tokens int32[R], rank int32[R] <- how many tokens have a larger logit, entropy fp32[R], lse fp32[R] <- the
     log of the sum of exp(scale * logits), top_ids int32[R, top] and top_logprobs fp32[R, top] <- the likeliest
-    tokens: those of them that are given. workspace: a uint8 tensor of logprobs_workspace_bytes."""
+    tokens: those of them that are given. scale: at least V * 2^-121. workspace: a uint8 tensor of
+    logprobs_workspace_bytes."""
     T = _names()
     dev = T.device()
     kind, (row, _) = _plain(logits, "logits", 2, dev, T)

@@ -478,6 +478,10 @@ static bool logits_fit(int64_t R, int64_t V, int top)
     return R >= 0 && R <= INT32_MAX / 64 && V >= 1 && V < (int64_t)1 << 30 && top >= 0 && top <= PN_LOGPROBS_MAX_TOP;
 }
 
+// Scales with which the sum of e^(s d) d stays within fp32: e^(s d) |d| is at most 0.37 / s and, where it is not zero, |d| at
+// most 128 / s, which V times are 2^128 at most. (A d that passes fp32 then has e^(s d) = 0, as it should.)
+static bool scale_fits(float scale, int64_t V) { return scale >= (float)V * 0x1p-121f && scale <= FLT_MAX; }
+
 }  // namespace pn
 
 using namespace pn;
@@ -498,7 +502,7 @@ extern "C" int pn_logprobs(const pn_logprobs_args *a, void *workspace, int64_t w
     const int size = elem_bytes(a->type);
     if (size == 0)
         return PN_ERR_FORMAT;
-    if (!logits_fit(a->R, a->V, a->top) || !(a->scale > 0.0f && a->scale <= FLT_MAX))
+    if (!logits_fit(a->R, a->V, a->top) || !scale_fits(a->scale, a->V))
         return PN_ERR_SHAPE;
     if (a->R == 0)
         return PN_OK;

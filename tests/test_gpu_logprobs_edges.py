@@ -63,3 +63,15 @@ def test_differences_past_fp32(env, type_, scale):
         same(got, t.double().numpy(), tokens, scale, 50)
     else:
         assert bool((got["logprob"][[0, 2]] == -float("inf")).all()) and bool((got["top_ids"][0, :2].cpu() == torch.tensor([3, 0])).all())
+
+
+@pytest.mark.parametrize("V,scale", [(1, 2.0 ** -121), (7001, 2.7e-33), (70001, 2.7e-32)])
+def test_smallest_scales(env, V, scale):
+    """Logits as large as such a scale makes ordinary."""
+    pn, torch, dev = env
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy((3 / scale * rng.normal(size=(4, V))).clip(-3e38, 3e38).astype(np.float32))
+    tokens = rng.integers(0, V, size=4).astype(np.int32)
+    got = call(pn, torch, x.to(dev), torch.from_numpy(tokens).to(dev), scale, min(V, 9))
+    torch.cuda.synchronize()
+    same(got, x.double().numpy(), tokens, scale, min(V, 9))
