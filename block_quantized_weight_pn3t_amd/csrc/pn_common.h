@@ -222,6 +222,10 @@ inline bool lds_limit_once(int bytes)
     return ok;
 }
 
+// Workgroups of `threads` threads that one launch takes. HIP counts a grid's threads in 32 bits: of more it runs what is left
+// modulo 2^32, without an error.
+constexpr int64_t launch_most(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 // Maps the launch status of the last kernel to PN_OK / PN_ERR_HIP.
 int launch_status();
 

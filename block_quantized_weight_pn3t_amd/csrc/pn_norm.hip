@@ -17,6 +17,8 @@
 // bits 99; 4095 of 17408 bf16 to 8-bit rows 45 us (4.8); four of 5120 fp32 4.1 us.
 #include <float.h>
 
+#include <algorithm>
+
 #include "pn_cache.h"
 #include "pn_lanes.h"
 
@@ -286,15 +288,36 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A)
     }
 }
 
-template <int T, int MODE, int NV, bool WAVE>
-static void launch_norm(const NormArgs &A, int pieces, hipStream_t s)
+// A's rows from `first` on.
+template <int T>
+static NormArgs rows_from(NormArgs A, int64_t first)
 {
-    const int per = WAVE ? 4 : 1, threads = ((pieces + NV - 1) / NV + 63) / 64 * 64;
-    const dim3 grid((unsigned)((A.rows + per - 1) / per)), block(WAVE ? 256 : threads);
-    if (A.K % VEC == 0)
-        hipLaunchKernelGGL((norm_kernel<T, MODE, NV, WAVE, true>), grid, block, 0, s, A);
-    else
-        hipLaunchKernelGGL((norm_kernel<T, MODE, NV, WAVE, false>), grid, block, 0, s, A);
+    typedef typename Elem<T>::type E;
+    const auto from = [first](auto *p, int64_t stride) { return p ? p + first * stride : p; };
+    A.rows -= first;
+    A.x = from((const E *)A.x, A.x_stride);
+    A.residual = from((const E *)A.residual, A.residual_stride);
+    A.sum = from((E *)A.sum, A.sum_stride);
+    A.out = from((E *)A.out, A.out_stride);
+    A.codes = from(A.codes, A.K);
+    A.scales = from(A.scales, 1);
+    return A;
+}
+
+template <int T, int MODE, int NV, bool WAVE>
+static void launch_norm(NormArgs A, int pieces, hipStream_t s)
+{
+    const int per = WAVE ? 4 : 1, threads = WAVE ? 256 : ((pieces + NV - 1) / NV + 63) / 64 * 64;
+    const int64_t most = launch_most(threads) * per;
+    for (;; A = rows_from<T>(A, most)) {
+        const dim3 grid((unsigned)((std::min(A.rows, most) + per - 1) / per)), block(threads);
+        if (A.K % VEC == 0)
+            hipLaunchKernelGGL((norm_kernel<T, MODE, NV, WAVE, true>), grid, block, 0, s, A);
+        else
+            hipLaunchKernelGGL((norm_kernel<T, MODE, NV, WAVE, false>), grid, block, 0, s, A);
+        if (A.rows <= most)
+            return;
+    }
 }
 
 // A thread holds one piece where rows are few, for latency, or of fp32 (8192 rows of 5120, norm: one 120 us, two 128), and

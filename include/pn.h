@@ -367,7 +367,7 @@ int pn_verify(int type, const void *p, int64_t p_stride, const void *q, int64_t 
  *   code = rint((127 * t) / T), product and quotient in 64 bits, ties to even; scale = T / 127
  * and the row stands for code * scale. Every code is fixed by this rule. A row of zeros has codes and
  * a scale of zero; a row with a NaN or an infinity has zero codes and a scale of NaN.
- * 1 <= K <= PN_ROW_MAX_WIDTH (else PN_ERR_SHAPE). Rows of plain numbers may have any stride (in
+ * 1 <= K <= PN_ROW_MAX_WIDTH, at most 2^31 - 1 rows (else PN_ERR_SHAPE). Rows of plain numbers may have any stride (in
  * elements) and alignment of their element; 16-byte aligned ones are a little faster. */
 #define PN_ROW_MAX_WIDTH 65536
 

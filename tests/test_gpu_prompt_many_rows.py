@@ -1,0 +1,60 @@
+"""More rows than one launch takes (2^32 threads)."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import block_quantized_weight_pn3t_amd as pn
+    yield pn, torch, torch.device("cuda:0")
+    torch.cuda.empty_cache()
+
+
+def codes_of(torch, t):
+    """Codes and T of the 8-bit rows of t (64 bits)."""
+    top = t.abs().amax(-1, keepdim=True)
+    return torch.round(127.0 * t / torch.where(top > 0, top, 1.0)).to(torch.int8), top[:, 0]
+
+
+def test_norm_of_narrow_rows(env):
+    """A wave a row: every output of every row."""
+    pn, torch, dev = env
+    rows, K = (1 << 26) + 5, 8
+    x = torch.randn(rows, K, dtype=torch.bfloat16, device=dev)
+    residual = torch.randn(rows, K, dtype=torch.bfloat16, device=dev)
+    weight = torch.randn(K, device=dev).bfloat16()
+    total, out = torch.zeros_like(x), torch.zeros_like(x)
+    codes, scales = torch.zeros(rows, K, dtype=torch.int8, device=dev), torch.zeros(rows, device=dev)
+    pn.add_norm(x, weight, 1e-6, out=out, codes=codes, scales=scales, residual=residual, sum=total)
+    torch.cuda.synchronize()
+    for at in range(0, rows, 1 << 23):
+        part = slice(at, at + (1 << 23))
+        h = x[part] + residual[part]
+        assert torch.equal(total[part], h)
+        t = h.double() * weight.double()
+        r = 1.0 / torch.sqrt(h.double().square().mean(-1) + float(torch.tensor(1e-6)))
+        want, top = codes_of(torch, t)
+        assert torch.equal(codes[part], want)
+        # one rounding of what 64 bits give to fp32, and to bf16
+        s, y = top * r / 127.0, t * r[:, None]
+        assert bool(((scales[part].double() - s).abs() <= 2.0 ** -24 * 1.000001 * s).all())
+        assert bool(((out[part].double() - y).abs() <= (2.0 ** -8 + 2.0 ** -23) * y.abs()).all())
+
+
+def test_rows_of_a_workgroup_each(env):
+    """Rows that overlap in memory, each of 192 threads."""
+    pn, torch, dev = env
+    rows, K = (1 << 32) // 192 + 7, 1032
+    base = torch.randn(rows + K - 1, device=dev).bfloat16()
+    x = base.as_strided((rows, K), (1, 1))
+    codes, scales = torch.zeros(rows, K, dtype=torch.int8, device=dev), torch.zeros(rows, device=dev)  # 23 GB
+    pn.int8_quantize_rows(x, codes, scales)
+    torch.cuda.synchronize()
+    top = torch.nn.functional.max_pool1d(base.float().abs()[None, None], K, 1)[0, 0]
+    assert torch.equal(scales, (top.double() / 127.0).float())
+    for at in (0, rows // 2, (1 << 32) // 192 - 2000, rows - 4000):
+        assert torch.equal(codes[at:at + 4000], codes_of(torch, x[at:at + 4000].double())[0])
