@@ -459,18 +459,38 @@ static int log_groups(int64_t R, int batches)
     return (int)std::max<int64_t>(1, std::min<int64_t>({64, (batches + waves - 1) / waves, (waves == 4 ? 1024 : 256) / R}));
 }
 
+// A's rows from `first` on, of a workgroup each.
 template <int T>
-static int launch_log(const LogArgs &A, int64_t R, hipStream_t s)
+static LogArgs rows_from(LogArgs A, int64_t first)
 {
-    const dim3 grid((unsigned)(R * A.groups));
+    const auto from = [first](auto *p, int64_t stride) { return p ? p + first * stride : p; };
+    A.logits = from((const typename Elem<T>::type *)A.logits, A.stride);
+    A.tokens = from(A.tokens, 1);
+    A.logprob = from(A.logprob, 1);
+    A.rank = from(A.rank, 1);
+    A.entropy = from(A.entropy, 1);
+    A.lse = from(A.lse, 1);
+    A.top_ids = from(A.top_ids, A.top);
+    A.top_logprobs = from(A.top_logprobs, A.top);
+    return A;
+}
+
+template <int T>
+static int launch_log(LogArgs A, int64_t R, hipStream_t s)
+{
     const int waves = log_waves(R, A.batches);
-    if (waves == 16)
-        hipLaunchKernelGGL((logprobs_kernel<T, 16>), grid, dim3(1024), 0, s, A);
-    else if (waves == 8)
-        hipLaunchKernelGGL((logprobs_kernel<T, 8>), grid, dim3(512), 0, s, A);
-    else
-        hipLaunchKernelGGL((logprobs_kernel<T, 4>), grid, dim3(256), 0, s, A);
-    return launch_status();
+    const int64_t most = launch_most(64 * waves);  // rows share workgroups where there are far fewer
+    for (;; A = rows_from<T>(A, most), R -= most) {
+        const dim3 grid((unsigned)(std::min(R, most) * A.groups));
+        if (waves == 16)
+            hipLaunchKernelGGL((logprobs_kernel<T, 16>), grid, dim3(1024), 0, s, A);
+        else if (waves == 8)
+            hipLaunchKernelGGL((logprobs_kernel<T, 8>), grid, dim3(512), 0, s, A);
+        else
+            hipLaunchKernelGGL((logprobs_kernel<T, 4>), grid, dim3(256), 0, s, A);
+        if (R <= most)
+            return launch_status();
+    }
 }
 
 static bool logits_fit(int64_t R, int64_t V, int top)

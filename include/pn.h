@@ -464,7 +464,7 @@ int pn_cache_append(const pn_cache *cache, const pn_append_args *a, void *stream
  * with a NaN or +infinity has NaN in every output but rank and top_ids, which go by comparisons (a NaN
  * is neither counted nor among the top).
  * Maxima, exponentials and sums in fp32 relative to a row's running maximum. Deterministic.
- * 1 <= V < 2^30, 0 <= top <= PN_LOGPROBS_MAX_TOP, scale finite and at least V * 2^-121, with which no sum of
+ * R < 2^25, 1 <= V < 2^30, 0 <= top <= PN_LOGPROBS_MAX_TOP, scale finite and at least V * 2^-121, with which no sum of
  * a row's differences leaves fp32 (else PN_ERR_SHAPE).
  * workspace: pn_logprobs_workspace_bytes of device memory (16-byte aligned), with any content to
  * begin with, overwritten; calls that may overlap need one each. Enough for fewer rows, a smaller V

@@ -58,3 +58,25 @@ def test_rows_of_a_workgroup_each(env):
     assert torch.equal(scales, (top.double() / 127.0).float())
     for at in (0, rows // 2, (1 << 32) // 192 - 2000, rows - 4000):
         assert torch.equal(codes[at:at + 4000], codes_of(torch, x[at:at + 4000].double())[0])
+
+
+def test_logprobs_of_many_rows(env):
+    pn, torch, dev = env
+    R, V, top = (1 << 24) + 5, 3, 2
+    x = torch.randn(R, V, device=dev)
+    tokens = torch.randint(0, V, (R,), dtype=torch.int32, device=dev)
+    got = dict(logprob=torch.zeros(R, device=dev), rank=torch.full((R,), 9, dtype=torch.int32, device=dev),
+               entropy=torch.zeros(R, device=dev), lse=torch.zeros(R, device=dev),
+               top_ids=torch.full((R, top), 9, dtype=torch.int32, device=dev), top_logprobs=torch.zeros(R, top, device=dev))
+    work = torch.empty(pn.logprobs_workspace_bytes(R, V, top), dtype=torch.uint8, device=dev)
+    pn.logprobs(x, tokens, workspace=work, **got)
+    torch.cuda.synchronize()
+    at = tokens.long()[:, None]
+    assert torch.equal(got["rank"], (x > x.gather(1, at)).sum(-1).int())
+    order = torch.sort(x, stable=True, dim=-1, descending=True)[1][:, :top]
+    assert torch.equal(got["top_ids"].long(), order)
+    p = torch.log_softmax(x.double(), -1)
+    # each of a few roundings of numbers of up to some 15
+    for name, want in (("logprob", p.gather(1, at)[:, 0]), ("entropy", -(p.exp() * p).sum(-1)),
+                       ("lse", torch.logsumexp(x.double(), -1)), ("top_logprobs", p.gather(1, order))):
+        assert float((got[name].double() - want).abs().max()) <= 2.0 ** -24 * 400, name
