@@ -576,7 +576,8 @@ __global__ void __launch_bounds__(512, 2) gemm_int8_large_kernel(GemmArgs A)
 static bool gemm_fit(int64_t M, int64_t N, int64_t K)
 {
     return M >= 0 && N >= 0 && M <= INT32_MAX && N <= INT32_MAX && K >= 16 && K % 16 == 0 && K <= PN_GEMM_INT8_MAX_K &&
-           ((M + 63) / 64) * ((N + 63) / 64) <= INT32_MAX / 64;
+           ((M + 63) / 64) * ((N + 63) / 64) <= INT32_MAX / 64 &&
+           ((M + 255) / 256) * ((N + 255) / 256) <= launch_most(512);  // so that tiles of 256 can always be launched
 }
 
 // How a product is cut.
@@ -607,7 +608,7 @@ static GemmCut gemm_cut(int64_t M, int64_t N, int64_t K)
         const double edge = size == 64 ? 2.3 : size == 128 ? 5.2 : 10.0;
         for (int splits = 1; splits <= (size == 256 ? 1 : std::min<int64_t>(8, lines / 4 + 1)); splits++) {
             const int64_t each = up(lines, splits), blocks = t * splits;
-            if (up(lines, each) != splits || (splits > 1 && blocks > 2 * slots))
+            if (up(lines, each) != splits || (splits > 1 && blocks > 2 * slots) || blocks > launch_most(size == 256 ? 512 : 256))
                 continue;
             const double line = size == 64 ? (blocks <= cus ? 0.25 : 0.38) : size == 128 ? 0.5 : 0.92;
             const double join = splits == 1 ? 0.0 : size == 64 ? 2.3 + 0.6 * splits : 1.45 * splits;

@@ -408,7 +408,8 @@ int pn_add_norm(const pn_add_norm_args *a, void *stream);
  * (codes from -128 on), out of `type` (PN_F32, PN_BF16, PN_F16). The sum is exact; it is converted to
  * fp32, multiplied by a_scales[m], then by w_scales[n] in fp32 and rounded to its type: three
  * roundings of 2^-24 and the type's. K a positive multiple of 16, at most PN_GEMM_INT8_MAX_K (sums
- * stay below 2^31; else PN_ERR_SHAPE); M and N below 2^31. a and w 16-byte aligned.
+ * stay below 2^31; else PN_ERR_SHAPE); M and N below 2^31, with fewer than 2^25 tiles of 64 x 64 outputs
+ * and 2^23 of 256 x 256 (else PN_ERR_SHAPE). a and w 16-byte aligned.
  * Deterministic. workspace: pn_gemm_int8_workspace_bytes of device memory (16-byte aligned), with any
  * content to begin with, overwritten; calls that may overlap need one each. Fewer rows can need more
  * of it: for calls of several sizes take the largest. */

@@ -80,3 +80,20 @@ def test_logprobs_of_many_rows(env):
     for name, want in (("logprob", p.gather(1, at)[:, 0]), ("entropy", -(p.exp() * p).sum(-1)),
                        ("lse", torch.logsumexp(x.double(), -1)), ("top_logprobs", p.gather(1, order))):
         assert float((got[name].double() - want).abs().max()) <= 2.0 ** -24 * 400, name
+
+
+def test_product_of_many_rows(env):
+    """More tiles of 64 than one launch takes."""
+    pn, torch, dev = env
+    M, N, K = (1 << 30) + 3, 2, 16
+    a = torch.randint(-128, 128, (M, K), dtype=torch.int8, device=dev)  # 17 GB
+    w = torch.randint(-128, 128, (N, K), dtype=torch.int8, device=dev)
+    sa, sw = torch.rand(M, device=dev), torch.rand(N, device=dev)
+    out = torch.full((M, N), 7.0, device=dev)
+    work = torch.empty(pn.gemm_int8_workspace_bytes(M, N, K), dtype=torch.uint8, device=dev)
+    pn.gemm_int8(a, sa, w, sw, out, work)
+    torch.cuda.synchronize()
+    for at in range(0, M, 1 << 26):
+        part = slice(at, at + (1 << 26))
+        sums = torch.matmul(a[part].float(), w.float().t())  # whole numbers below 2^24
+        assert torch.equal(out[part], sums * sa[part, None] * sw)
