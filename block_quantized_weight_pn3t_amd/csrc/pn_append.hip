@@ -304,7 +304,7 @@ extern "C" int pn_cache_append(const pn_cache *cache, const pn_append_args *a, v
     const int size = elem_bytes(a->type);
     if (size == 0)
         return PN_ERR_FORMAT;
-    if (a->T < 0 || !tokens_fit(a->T, c.heads) || a->rows < 1 || a->rot < 8 || a->rot % 8 || a->rot > cache->dim ||
+    if (a->T < 0 || !tokens_fit(a->T, c.heads, kQuads * 4) || a->rows < 1 || a->rot < 8 || a->rot % 8 || a->rot > cache->dim ||
         (a->interleaved != 0 && a->interleaved != 1) || (!a->positions && a->rows < a->T) || (a->q && a->Hq < 1))
         return PN_ERR_SHAPE;
     if (a->T == 0)
@@ -353,7 +353,7 @@ extern "C" int pn_cache_append(const pn_cache *cache, const pn_append_args *a, v
             return PN_ERR_SHAPE;
         blocks += runs * A.head_blocks;
     }
-    if (blocks > INT32_MAX)
+    if (blocks > launch_most(256))
         return PN_ERR_SHAPE;
     if ((st = check_device()) != PN_OK)
         return st;

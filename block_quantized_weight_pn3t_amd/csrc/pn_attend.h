@@ -1166,8 +1166,6 @@ static int launch_attend(const AttendArgs &A, hipStream_t s)
     const int64_t rows = (int64_t)A.B * A.Q * A.Hq;
     const int64_t grid = (int64_t)A.c.heads * A.prefix_splits * A.prefix_blocks +
                          (int64_t)A.own_splits * A.B * A.own_blocks * A.c.heads;
-    if (grid > INT32_MAX || rows > INT32_MAX / (D / 64))
-        return PN_ERR_SHAPE;
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kWaves * 64), bytes, s, A);
     const int st = launch_status();
     if (st != PN_OK || A.direct)

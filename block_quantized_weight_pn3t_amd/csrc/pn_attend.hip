@@ -112,6 +112,12 @@ extern "C" int pn_attend(const pn_cache *cache, const pn_attend_args *a, void *w
     if (c.pages == 0 && (a->table_width > 0 || a->prefix_len > 0))
         return PN_ERR_SHAPE;  // no page to read
     const Cut t = attend_cut(cache, a);
+    // workgroups of both kernels
+    const int64_t grid = (int64_t)c.heads * t.prefix_splits * t.prefix_blocks +
+                         (int64_t)t.own_splits * a->B * t.own_blocks * c.heads;
+    if (grid > launch_most(kWaves * 64) || t.rows > INT32_MAX / (cache->dim / 64) ||
+        (!t.direct && t.rows > launch_most(cache->dim / 4) - 256))
+        return PN_ERR_SHAPE;
     if (t.workspace > 0) {
         if (!workspace)
             return PN_ERR_NULL;

@@ -225,7 +225,7 @@ extern "C" int pn_cache_write(const pn_cache *cache, int type, const void *k, in
     const int size = elem_bytes(type);
     if (size == 0)
         return PN_ERR_FORMAT;
-    if (T < 0 || !tokens_fit(T, c.heads))
+    if (T < 0 || !tokens_fit(T, c.heads, kQuads * 4))
         return PN_ERR_SHAPE;
     if (T == 0)
         return PN_OK;
@@ -253,7 +253,7 @@ extern "C" int pn_cache_read(const pn_cache *cache, int type, const int64_t *slo
     const int size = elem_bytes(type);
     if (size == 0)
         return PN_ERR_FORMAT;
-    if (T < 0 || !tokens_fit(T, c.heads))
+    if (T < 0 || !tokens_fit(T, c.heads, 16))
         return PN_ERR_SHAPE;
     if (T == 0)
         return PN_OK;

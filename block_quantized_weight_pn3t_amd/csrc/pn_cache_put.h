@@ -175,10 +175,10 @@ inline int by_kind(int fmt, int dim, int type, F f)
     return PN_ERR_SHAPE;
 }
 
-// Tokens of one call: its token quads and heads are counted in 32 bits.
-inline bool tokens_fit(int64_t ntok, int heads)
+// Tokens of one call, `each` of them and a head a workgroup of 256 threads: what one launch takes.
+inline bool tokens_fit(int64_t ntok, int heads, int each)
 {
-    return ntok <= (int64_t)1 << 40 && (ntok + 3) / 4 * heads < INT32_MAX;
+    return ntok <= (int64_t)1 << 40 && (ntok + each - 1) / each * heads <= launch_most(256);
 }
 
 }  // namespace pn

@@ -311,6 +311,8 @@ static int launch_nv(const uint8_t *codes, const uint8_t *scales, float g, int64
     if (!lds_limit_once<kern>(kNvLdsBudget))
         return PN_ERR_HIP;
     const int64_t rows_per_wg = 4 * R;
+    if (N > launch_most(256) * rows_per_wg)
+        return PN_ERR_SHAPE;
     hipLaunchKernelGGL(kern, dim3((unsigned)((N + rows_per_wg - 1) / rows_per_wg)), dim3(256),
                        (size_t)phase_groups * per_group, s, codes, scales, g, N, K, x, y,
                        phase_groups);

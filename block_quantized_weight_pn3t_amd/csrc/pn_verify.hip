@@ -350,6 +350,11 @@ extern "C" int pn_verify(int type, const void *p, int64_t p_stride, const void *
         return PN_ERR_SHAPE;
     if (B == 0)
         return PN_OK;
+    // enough workgroups to fill the memory pipe, few enough to arrive soon
+    const int64_t chunks = verify_chunks(V);
+    const int groups = (int)std::min<int64_t>(chunks, std::min<int64_t>(64, std::max<int64_t>(16, 1024 / B)));
+    if (B > launch_most(256) / groups)
+        return PN_ERR_SHAPE;
     if (!p || !u_sample || !tokens || !accepted || !workspace || (K > 0 && (!draft || !u_accept)))
         return PN_ERR_NULL;
     if (!aligned(p, size) || !aligned(q, size) || !aligned(draft, 4) || !aligned(n_draft, 4) ||
@@ -361,9 +366,6 @@ extern "C" int pn_verify(int type, const void *p, int64_t p_stride, const void *
     const int st = check_device();
     if (st != PN_OK)
         return st;
-    // enough workgroups to fill the memory pipe, few enough to arrive soon
-    const int64_t chunks = verify_chunks(V);
-    const int groups = (int)std::min<int64_t>(chunks, std::min<int64_t>(64, std::max<int64_t>(16, 1024 / B)));
     const VerifyArgs A{p, q, p_stride, q_stride, draft, n_draft, u_accept, u_sample, V, (int)K,
                        (int)chunks, groups, tokens, accepted, call_number(),
                        (unsigned long long *)workspace, (double2 *)((char *)workspace + B * kLine * 8)};

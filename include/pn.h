@@ -20,7 +20,8 @@
  *   - The return value is a status (PN_OK = 0, or a negative PN_ERR_*), decided synchronously from
  *     the arguments and the launch. Per-row verdicts and quantizer statuses are device outputs.
  *   - Nothing falls back silently: a shape, dtype or device this library does not handle is an
- *     error, never a slower path on another device.
+ *     error, never a slower path on another device. Sizes that a launch does not take (fewer than 2^32
+ *     threads) are PN_ERR_SHAPE where a call is not made in several launches.
  *   - N == 0, nrows == 0 or M == 0 is a no-op that returns PN_OK. K must be a positive whole
  *     number of blocks (80 for pn3t, 64 for pn4t, 16 for NVFP4); otherwise PN_ERR_SHAPE.
  *
@@ -272,14 +273,15 @@ int64_t pn_cache_page_bytes(int format, int heads, int dim, int page);
  * contiguous, token t and head h at element t * token_stride + h * head_stride. slots int64[T] on
  * the device: token t goes to place slots[t] % page of page slots[t] / page; a slot outside
  * 0 .. pages * page - 1 (a padding token's -1) writes nothing. Slots of one call must differ. k and
- * v need only their element's alignment (4 elements' alignment of bases and strides is faster). */
+ * v need only their element's alignment (4 elements' alignment of bases and strides is faster).
+ * T / 32, rounded up, times heads is below 2^24 (else PN_ERR_SHAPE). */
 int pn_cache_write(const pn_cache *cache, int type, const void *k, int64_t k_token_stride,
                    int64_t k_head_stride, const void *v, int64_t v_token_stride,
                    int64_t v_head_stride, const int64_t *slots, int64_t T, void *stream);
 
 /* Reads T tokens back: k and v [T][heads][dim] of `type`, contiguous, aligned to 4 elements: the
  * numbers above, exact in fp32 and bf16, rounded once to fp16. A slot outside the cache gives
- * zeros. Slots may repeat. */
+ * zeros. Slots may repeat. T / 16, rounded up, times heads is below 2^24 (else PN_ERR_SHAPE). */
 int pn_cache_read(const pn_cache *cache, int type, const int64_t *slots, int64_t T, void *k, void *v,
                   void *stream);
 
@@ -429,7 +431,9 @@ int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t
  * the cache is fixed; values are quantised as they are. Queries are turned likewise, rounded to fp32 and
  * to their type.
  * A token whose slot is outside the cache writes no key and no value; its queries are turned all the
- * same. A position outside the table is taken as the nearest row inside it. */
+ * same. A position outside the table is taken as the nearest row inside it.
+ * T / 32, rounded up, times heads, and with it what the queries need (a workgroup for a few thousand of their
+ * numbers), is below 2^24 (else PN_ERR_SHAPE). */
 typedef struct pn_append_args {
     int type;                /* of q, q_out, k and v: PN_F32, PN_BF16 or PN_F16 */
     int Hq;                  /* query heads, 1 or more where q is given; need not be a multiple of cache->heads */

@@ -97,3 +97,16 @@ def test_product_of_many_rows(env):
         part = slice(at, at + (1 << 26))
         sums = torch.matmul(a[part].float(), w.float().t())  # whole numbers below 2^24
         assert torch.equal(out[part], sums * sa[part, None] * sw)
+
+
+def test_nvfp4_rows_that_no_launch_takes(env):
+    """One token that is not 16-byte aligned: a workgroup for eight rows, 2^24 of them."""
+    pn, torch, dev = env
+    N, K = 1 << 27, 16
+    codes, scales = torch.zeros(N, K // 2, dtype=torch.uint8, device=dev), torch.zeros(N, 1, dtype=torch.uint8, device=dev)
+    x, y = torch.zeros(K + 1, dtype=torch.bfloat16, device=dev)[1:], torch.zeros(1, N, device=dev)
+    call = pn.lib().pn_gemv_nvfp4
+    args = lambda n: (codes.data_ptr(), scales.data_ptr(), 1.0, n, K, x.data_ptr(), 1, y.data_ptr(), None)  # noqa: E731
+    torch.cuda.synchronize()
+    assert call(*args(N)) == -2 and call(*args(N - 8)) == 0
+    torch.cuda.synchronize()

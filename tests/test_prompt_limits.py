@@ -6,7 +6,7 @@ import pytest
 import torch  # first: the library takes its HIP runtime
 
 import block_quantized_weight_pn3t_amd as pn
-from test_prompt_reference import gemm, logp
+from test_prompt_reference import append, cache_desc, gemm, logp
 
 
 @pytest.mark.parametrize("V,scale,refused", [
@@ -23,3 +23,32 @@ def test_logprobs_scales(V, scale, refused):
 def test_gemm_int8_tiles(M, N, refused):
     """Outputs of which one launch has tiles of 256 for all."""
     assert (gemm(M=M, N=N, K=16, a=C.c_void_p(0x1008)) == -2) == refused
+
+
+def test_launches_of_the_cache():
+    """2^24 workgroups of 256 threads are one too many for a launch. (The alignment is looked at after the sizes.)"""
+    odd, fake = C.c_void_p(0x1001), C.c_void_p(0x1000)
+    for T, heads, write, read in ((8192 - 32, 65536, False, True), (8192 - 31, 65536, True, True), (4096 - 16, 65536, False, False),
+                                  (4096 - 15, 65536, False, True), (1 << 29, 1, True, True), ((1 << 29) - 32, 1, False, True)):
+        c = cache_desc(heads=heads)
+        assert (pn.lib().pn_cache_write(c, 0, odd, 0, 0, fake, 0, 0, fake, T, None) == -2) == write, (T, heads)
+        assert (pn.lib().pn_cache_read(c, 0, fake, T, odd, fake, None) == -2) == read, (T, heads)
+        assert (append(c, T=T, q=0, k=0x1001) == -2) == write, (T, heads)
+
+
+def test_launches_of_the_queries():
+    assert append(cache_desc(heads=1), T=1 << 20, Hq=1 << 16, positions=0x1000, rows=1) == -2
+
+
+def test_launches_of_attention_and_verification():
+    import test_step_reference as step
+    fake = C.c_void_p(0x1000)
+
+    def attend(B, **kw):
+        a = step.attend_args(pn, B=B, Q=1, Hq=2, prefix_len=0, table_width=1, **kw)
+        return pn.lib().pn_attend(C.byref(step.desc(pn, heads=2)), C.byref(a), None, 0, None)
+    # two heads of eight waves a sequence; a missing workspace is looked at after the sizes
+    assert attend(1 << 22) == -2
+    for B, V, refused in ((1 << 20, 32768, True), ((1 << 20) - 1, 32768, False), (1 << 24, 100, True), ((1 << 24) - 1, 100, False)):
+        st = pn.lib().pn_verify(0, fake, V, None, V, None, None, None, C.c_void_p(0x1002), B, 0, V, fake, fake, fake, 1 << 50, None)
+        assert (st == -2) == refused, (B, V)
