@@ -238,15 +238,16 @@ int pn_validate_rows(int type, const void *W, int64_t nrows, int64_t K, int32_t 
         return st;
     const int nb = (int)(K / pn_group(type));
     const int64_t rb = pn_row_bytes(type, K);
-    const dim3 grid((unsigned)((nrows + 3) / 4)), block(256);
     hipStream_t s = (hipStream_t)stream;
-    if (type == PN_TYPE_PN3T)
-        hipLaunchKernelGGL(validate_kernel<PN_TYPE_PN3T>, grid, block, 0, s,
-                           (const uint8_t *)W, nrows, nb, rb, verdict);
-    else
-        hipLaunchKernelGGL(validate_kernel<PN_TYPE_PN4T>, grid, block, 0, s,
-                           (const uint8_t *)W, nrows, nb, rb, verdict);
-    return launch_status();
+    return launch_rows(nrows, 64, [&](int64_t first, int64_t rows, dim3 grid) {
+        const uint8_t *const at = (const uint8_t *)W + first * rb;
+        if (type == PN_TYPE_PN3T)
+            hipLaunchKernelGGL(validate_kernel<PN_TYPE_PN3T>, grid, dim3(256), 0, s, at, rows, nb, rb,
+                               verdict + first);
+        else
+            hipLaunchKernelGGL(validate_kernel<PN_TYPE_PN4T>, grid, dim3(256), 0, s, at, rows, nb, rb,
+                               verdict + first);
+    });
 }
 
 int pn_validate_row(int type, const void *row, int64_t K, int32_t *verdict, void *stream)
@@ -261,16 +262,16 @@ int pn_dequantize_rows(int type, const void *W, int64_t nrows, int64_t K, float 
         return st;
     const int nb = (int)(K / pn_group(type));
     const int64_t rb = pn_row_bytes(type, K);
-    const int64_t total = nrows * nb * 8;
-    const dim3 grid((unsigned)((total + 255) / 256)), block(256);
     hipStream_t s = (hipStream_t)stream;
-    if (type == PN_TYPE_PN3T)
-        hipLaunchKernelGGL(dequantize_kernel<PN_TYPE_PN3T>, grid, block, 0, s,
-                           (const uint8_t *)W, nrows, nb, rb, out);
-    else
-        hipLaunchKernelGGL(dequantize_kernel<PN_TYPE_PN4T>, grid, block, 0, s,
-                           (const uint8_t *)W, nrows, nb, rb, out);
-    return launch_status();
+    return launch_rows(nrows, (int64_t)nb * 8, [&](int64_t first, int64_t rows, dim3 grid) {
+        const uint8_t *const at = (const uint8_t *)W + first * rb;
+        if (type == PN_TYPE_PN3T)
+            hipLaunchKernelGGL(dequantize_kernel<PN_TYPE_PN3T>, grid, dim3(256), 0, s, at, rows, nb, rb,
+                               out + first * K);
+        else
+            hipLaunchKernelGGL(dequantize_kernel<PN_TYPE_PN4T>, grid, dim3(256), 0, s, at, rows, nb, rb,
+                               out + first * K);
+    });
 }
 
 int pn_dequantize_row(int type, const void *row, int64_t K, float *out, void *stream)
@@ -298,9 +299,10 @@ int pn_nvfp4_validate_rows(const uint8_t *scales, float g, int64_t N, int64_t K,
     if ((st = check_device()) != PN_OK)
         return st;
     const int gok = (g > 0.0f && g <= 3.402823466e38f) ? 1 : 0;  // finite and positive
-    hipLaunchKernelGGL(nvfp4_validate_kernel, dim3((unsigned)((N + 3) / 4)), dim3(256), 0,
-                       (hipStream_t)stream, scales, gok, N, (int)(K / 16), verdict);
-    return launch_status();
+    return launch_rows(N, 64, [&](int64_t first, int64_t rows, dim3 grid) {
+        hipLaunchKernelGGL(nvfp4_validate_kernel, grid, dim3(256), 0, (hipStream_t)stream,
+                           scales + first * (K / 16), gok, rows, (int)(K / 16), verdict + first);
+    });
 }
 
 int pn_nvfp4_dequantize_rows(const uint8_t *codes, const uint8_t *scales, float g, int64_t N,
@@ -315,10 +317,10 @@ int pn_nvfp4_dequantize_rows(const uint8_t *codes, const uint8_t *scales, float 
         return PN_ERR_ALIGN;
     if ((st = check_device()) != PN_OK)
         return st;
-    const int64_t total = N * (K / 2);
-    hipLaunchKernelGGL(nvfp4_dequantize_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256),
-                       0, (hipStream_t)stream, codes, scales, g, N, K, out);
-    return launch_status();
+    return launch_rows(N, K / 2, [&](int64_t first, int64_t rows, dim3 grid) {
+        hipLaunchKernelGGL(nvfp4_dequantize_kernel, grid, dim3(256), 0, (hipStream_t)stream,
+                           codes + first * (K / 2), scales + first * (K / 16), g, rows, K, out + first * K);
+    });
 }
 
 }  // extern "C"

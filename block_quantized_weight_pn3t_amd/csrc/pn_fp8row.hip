@@ -411,9 +411,10 @@ extern "C" int pn_fp8row_validate_rows(const uint8_t *codes, const uint16_t *sca
     if ((st = check_device()) != PN_OK)
         return st;
     const int vec16 = (K % 16 == 0 && aligned(codes, 16)) ? 1 : 0;
-    hipLaunchKernelGGL(fp8row_validate_kernel, dim3((unsigned)((N + 3) / 4)), dim3(256), 0,
-                       (hipStream_t)stream, codes, scales, N, K, verdict, vec16);
-    return launch_status();
+    return launch_rows(N, 64, [&](int64_t first, int64_t rows, dim3 grid) {
+        hipLaunchKernelGGL(fp8row_validate_kernel, grid, dim3(256), 0, (hipStream_t)stream, codes + first * K,
+                           scales + first, rows, K, verdict + first, vec16);
+    });
 }
 
 extern "C" int pn_fp8row_dequantize_rows(const uint8_t *codes, const uint16_t *scales, int64_t N,
@@ -428,10 +429,10 @@ extern "C" int pn_fp8row_dequantize_rows(const uint8_t *codes, const uint16_t *s
         return PN_ERR_ALIGN;
     if ((st = check_device()) != PN_OK)
         return st;
-    const int64_t n = N * K;
-    hipLaunchKernelGGL(fp8row_dequantize_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                       (hipStream_t)stream, codes, scales, N, K, out);
-    return launch_status();
+    return launch_rows(N, K, [&](int64_t first, int64_t rows, dim3 grid) {
+        hipLaunchKernelGGL(fp8row_dequantize_kernel, grid, dim3(256), 0, (hipStream_t)stream, codes + first * K,
+                           scales + first, rows, K, out + first * K);
+    });
 }
 
 extern "C" int pn_gemv_fp8row(const uint8_t *codes, const uint16_t *scales, int64_t N, int64_t K,
