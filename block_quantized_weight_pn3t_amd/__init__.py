@@ -442,7 +442,7 @@ class Cache:
         if data.numel() % each:
             raise ValueError(f"data must be whole pages of {each} bytes, got {data.numel()}")
         self.format, self.heads, self.dim, self.page = format, heads, dim, page
-        self.pages, self.data = data.numel() // each, data
+        self.pages, self.data, self.device = data.numel() // each, data, data.get_device()
         self.desc = CacheDesc(format, heads, dim, page, self.pages, data.data_ptr())
         self.ref = C.addressof(self.desc)
 
@@ -739,6 +739,8 @@ def cache_append(cache, k, v, slots, rotation, positions=None, q=None, q_out=Non
     its own number unless given. interleaved: channels (2j, 2j + 1) turn together, not (j, j + rot / 2)."""
     T = _names()
     dev = T.device()
+    if cache.device != dev:
+        raise ValueError(f"the cache must be on the current device ({dev}), got {cache.data.device}")
     kind, (k_token, k_head, _) = _plain(k, "k", 3, dev, T)
     n, dt = k.shape[0], k.dtype
     shape = (n, cache.heads, cache.dim)

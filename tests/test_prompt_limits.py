@@ -52,3 +52,43 @@ def test_launches_of_attention_and_verification():
     for B, V, refused in ((1 << 20, 32768, True), ((1 << 20) - 1, 32768, False), (1 << 24, 100, True), ((1 << 24) - 1, 100, False)):
         st = pn.lib().pn_verify(0, fake, V, None, V, None, None, None, C.c_void_p(0x1002), B, 0, V, fake, fake, fake, 1 << 50, None)
         assert (st == -2) == refused, (B, V)
+
+
+class Lib:
+    """In the library's place: the names of the entry points that were called."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def on_host(monkeypatch):
+    """The binding with host tensors as those of the current device; its calls go nowhere."""
+    pn._names()
+    monkeypatch.setattr(pn._Torch, "device", staticmethod(lambda: -1))
+    monkeypatch.setattr(pn._Torch, "raw_stream", staticmethod(lambda device: 0))
+    lib = Lib()
+    monkeypatch.setattr(pn, "_lib", lib)
+    return lib
+
+
+def cache_on(device, heads=2, dim=64):
+    c = pn.Cache.__new__(pn.Cache)
+    c.format, c.heads, c.dim, c.page, c.pages, c.device, c.ref = pn.MXFP8, heads, dim, 32, 1, device, 0
+    c.data = torch.zeros(1, dtype=torch.uint8)
+    return c
+
+
+def test_append_to_a_cache_of_another_device(on_host):
+    k, slots, table = torch.zeros(3, 2, 64), torch.arange(3), torch.zeros(3, 64)
+    pn.cache_append(cache_on(-1), k, k, slots, table)
+    assert on_host.calls == ["pn_cache_append"]
+    with pytest.raises(ValueError, match="cache"):
+        pn.cache_append(cache_on(0), k, k, slots, table)
+    assert on_host.calls == ["pn_cache_append"]
