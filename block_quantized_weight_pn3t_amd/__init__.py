@@ -720,13 +720,25 @@ def gemm_int8(a, a_scales, w, w_scales, out, workspace=None, stream=None):
                              work_bytes, _handle(stream, T)), "pn_gemm_int8")
 
 
-def _heads(t, name, dtype, shape, dev):
-    """The token and head strides of t [T, heads, dim], channels contiguous."""
+def _overlap(n, heads, dim, token, head):
+    """Whether any of the dim numbers from t * token + h * head on belong to two (t < n, h < heads)."""
+    if n == 0 or ((heads < 2 or head >= dim) and (n < 2 or token >= (heads - 1) * head + dim)):
+        return False
+    for h in range(heads):  # the two tokens nearest to the head's distance, which begins and ends inside the tensor
+        t = h * head // token if token else 0
+        for t in (min(t, n - 1), min(t + 1, n - 1)):
+            if (t or h) and abs(t * token - h * head) < dim:
+                return True
+    return False
+
+
+def _heads(t, name, dtype, shape, dev, written=False):
+    """The token and head strides of t [T, heads, dim], channels contiguous; heads that are written must not overlap."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         token, head, channel = t.stride()
-        if channel == 1:
+        if channel == 1 and not (written and _overlap(*shape, token, head)):
             return token, head
-    _misfit(t, name, dtype, shape, dev, "a tensor with contiguous channels")
+    _misfit(t, name, dtype, shape, dev, "a tensor with contiguous channels" + " and heads that do not overlap" * written)
 
 
 _pack_append = struct.Struct("@iiPqqPqqPqqPqqPqiiPPq").pack  # pn_append_args
@@ -761,7 +773,7 @@ def cache_append(cache, k, v, slots, rotation, positions=None, q=None, q_out=Non
         hq = q.shape[1]
         shape = (n, hq, cache.dim)
         q_token, q_head = _heads(q, "q", dt, shape, dev)
-        out_token, out_head = _heads(q_out, "q_out", dt, shape, dev)
+        out_token, out_head = _heads(q_out, "q_out", dt, shape, dev, True)
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
     a = _pack_append(kind, hq, q_at, q_token, q_head, out_at, out_token, out_head, k.data_ptr(), k_token, k_head,
                      v.data_ptr(), v_token, v_head, rotation_at, rows, rot, 1 if interleaved else 0, positions_at,

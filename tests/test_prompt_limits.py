@@ -1,6 +1,7 @@
 """Limits of the prompt's entry points that are decided before anything runs: scales, sizes of launches, tensors that the
 binding is given."""
 import ctypes as C
+import itertools
 
 import pytest
 import torch  # first: the library takes its HIP runtime
@@ -92,3 +93,30 @@ def test_append_to_a_cache_of_another_device(on_host):
     with pytest.raises(ValueError, match="cache"):
         pn.cache_append(cache_on(0), k, k, slots, table)
     assert on_host.calls == ["pn_cache_append"]
+
+
+def test_overlaps_of_heads():
+    """Against the numbers' own places, for every small shape and stride."""
+    for n, heads, dim in itertools.product((0, 1, 2, 3, 4), (1, 2, 3), (1, 2, 4)):
+        for token, head in itertools.product(range(14), range(14)):
+            at = [t * token + h * head + d for t in range(n) for h in range(heads) for d in range(dim)]
+            assert pn._overlap(n, heads, dim, token, head) == (len(set(at)) < len(at)), (n, heads, dim, token, head)
+
+
+def test_append_to_queries_that_overlap(on_host):
+    k, slots, table = torch.zeros(3, 2, 64), torch.arange(3), torch.zeros(3, 64)
+    q = torch.zeros(3, 5, 64)
+    wide = torch.zeros(4096)
+    for q_out in (torch.zeros(3, 5, 64), torch.zeros(5, 3, 64).transpose(0, 1), torch.zeros(3, 9, 64)[:, 2:7], q,
+                  wide.as_strided((3, 5, 64), (5 * 64 + 1, 64, 1)), wide.as_strided((3, 5, 64), (128, 384, 1))):
+        pn.cache_append(cache_on(-1), k, k, slots, table, q=q, q_out=q_out)
+    # read as they are, from one head or token too
+    pn.cache_append(cache_on(-1), k, k, slots, table, q=q[:, :1].expand(3, 5, 64), q_out=q)
+    made = len(on_host.calls)
+    assert made == 7
+    for q_out in (torch.zeros(3, 1, 64).expand(3, 5, 64), torch.zeros(1, 5, 64).expand(3, 5, 64),
+                  wide.as_strided((3, 5, 64), (320, 63, 1)), wide.as_strided((3, 5, 64), (319, 64, 1)),
+                  wide.as_strided((3, 5, 64), (128, 256, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            pn.cache_append(cache_on(-1), k, k, slots, table, q=q, q_out=q_out)
+    assert len(on_host.calls) == made
