@@ -696,7 +696,7 @@ def add_norm(x, weight, eps, out=None, codes=None, scales=None, residual=None, s
 
 
 def gemm_int8_workspace_bytes(M, N, K):
-    """Device bytes that gemm_int8 needs for a [M, K] and w [N, K]."""
+    """Device bytes that gemm_int8 needs for a [M, K] and w [N, K]; enough for fewer rows of a, too."""
     return int(_lib.pn_gemm_int8_workspace_bytes(M, N, K))
 
 

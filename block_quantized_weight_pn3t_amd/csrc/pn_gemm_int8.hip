@@ -673,7 +673,15 @@ using namespace pn;
 
 extern "C" int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
-    return gemm_fit(M, N, K) && M > 0 && N > 0 ? gemm_cut(M, N, K).workspace : 0;
+    if (!gemm_fit(M, N, K) || M == 0 || N == 0 || K <= 3 * 128)
+        return 0;
+    // The most that any number of rows up to M takes, which all come down to multiples of 64: more rows can need less, as
+    // their tiles are enough without parts of K (none has parts from `whole` rows on).
+    const int64_t cus = device_cus(), whole = std::max(2 * cus / ((N + 63) / 64) * 64, cus / ((N + 127) / 128) * 128);
+    int64_t most = 0;
+    for (int64_t m = std::min(M, whole); m > 32; m = (m - 1) / 64 * 64)
+        most = std::max(most, gemm_cut(m, N, K).workspace);
+    return most;
 }
 
 extern "C" int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t *w,

@@ -413,8 +413,7 @@ int pn_add_norm(const pn_add_norm_args *a, void *stream);
  * stay below 2^31; else PN_ERR_SHAPE); M and N below 2^31, with fewer than 2^25 tiles of 64 x 64 outputs
  * and 2^23 of 256 x 256 (else PN_ERR_SHAPE). a and w 16-byte aligned.
  * Deterministic. workspace: pn_gemm_int8_workspace_bytes of device memory (16-byte aligned), with any
- * content to begin with, overwritten; calls that may overlap need one each. Fewer rows can need more
- * of it: for calls of several sizes take the largest. */
+ * content to begin with, overwritten; calls that may overlap need one each. Enough for fewer rows of a, too. */
 #define PN_GEMM_INT8_MAX_K 131056
 int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K); /* 0 where none is needed */
 

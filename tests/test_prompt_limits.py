@@ -120,3 +120,13 @@ def test_append_to_queries_that_overlap(on_host):
         with pytest.raises(ValueError, match="overlap"):
             pn.cache_append(cache_on(-1), k, k, slots, table, q=q, q_out=q_out)
     assert len(on_host.calls) == made
+
+
+@pytest.mark.parametrize("N,K", [(1, 17408), (64, 512), (200, 5120), (1024, 5120), (2560, 17408), (5120, 5120), (5120, 17408),
+                                 (10240, 1024), (34816, 5120), (1024, 384)])
+def test_gemm_int8_workspace_is_enough_for_fewer_rows(N, K):
+    need = [pn.gemm_int8_workspace_bytes(M, N, K) for M in [*range(0, 3000, 7), *range(3000, 70000, 997)]]
+    assert need == sorted(need)
+    assert need[4] == 0  # up to 32 rows take none
+    if K <= 384 or N > 32768:  # nor do short rows, or weights whose own tiles fill the machine
+        assert need[-1] == 0
