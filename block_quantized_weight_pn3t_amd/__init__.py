@@ -129,6 +129,7 @@ _SIGS = {
     "pn_int8_quantize_rows": (_I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P]),
     "pn_add_norm": (_I32, [_P, _P]),
     "pn_gemm_int8_workspace_bytes": (_I64, [_I64, _I64, _I64]),
+    "pn_gemm_int8_cut": (_I32, [_I64, _I64, _I64, _P]),
     "pn_gemm_int8": (_I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I32, _P, _I64, _P, _I64, _P]),
     "pn_cache_append": (_I32, [_P, _P, _P]),
     "pn_logprobs_workspace_bytes": (_I64, [_I64, _I64, _I32]),

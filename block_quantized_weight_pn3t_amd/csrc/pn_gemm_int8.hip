@@ -684,6 +684,16 @@ extern "C" int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
     return most;
 }
 
+extern "C" int pn_gemm_int8_cut(int64_t M, int64_t N, int64_t K, int *parts)
+{
+    if (!gemm_fit(M, N, K) || M == 0 || N == 0)
+        return PN_ERR_SHAPE;
+    const GemmCut c = gemm_cut(M, N, K);
+    if (parts)
+        *parts = c.splits;
+    return c.size;
+}
+
 extern "C" int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t *w,
                             const float *w_scales, int64_t N, int64_t K, int type, void *out,
                             int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream)

@@ -417,6 +417,11 @@ int pn_add_norm(const pn_add_norm_args *a, void *stream);
 #define PN_GEMM_INT8_MAX_K 131056
 int64_t pn_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K); /* 0 where none is needed */
 
+/* How such a product is made on the current device, for tests and profiles: 0 as a stream of w (up to 32
+ * rows of a), 64, 128 or 256 in square tiles of so many outputs, and in how many parts of K each (parts may be
+ * NULL). PN_ERR_SHAPE where there is none. Host-only. */
+int pn_gemm_int8_cut(int64_t M, int64_t N, int64_t K, int *parts);
+
 int pn_gemm_int8(const int8_t *a, const float *a_scales, int64_t M, const int8_t *w,
                  const float *w_scales, int64_t N, int64_t K, int type, void *out,
                  int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream);
