@@ -130,3 +130,14 @@ def test_gemm_int8_workspace_is_enough_for_fewer_rows(N, K):
     assert need[4] == 0  # up to 32 rows take none
     if K <= 384 or N > 32768:  # nor do short rows, or weights whose own tiles fill the machine
         assert need[-1] == 0
+
+
+@pytest.mark.parametrize("args,pack", [(pn.AddNormArgs, pn._pack_add_norm), (pn.AppendArgs, pn._pack_append),
+                                       (pn.LogprobsArgs, pn._pack_logprobs), (pn.AttendArgs, pn._pack_attend)])
+def test_packed_arguments_are_the_structures(args, pack):
+    """The calls pack by format strings what the structures name field by field."""
+    values = [0.5 + n if kind is C.c_float else n + 1 for n, (_, kind) in enumerate(args._fields_)]
+    packed = pack(*values)
+    assert len(packed) == C.sizeof(args)
+    fields = args.from_buffer_copy(packed)
+    assert [getattr(fields, name) for name, _ in args._fields_] == values
