@@ -1,6 +1,7 @@
 // pn_attend.hip -- pn_attend's arguments, how a call is cut into workgroups, and its entry points.
 // The kernels are in pn_attend.h.
 #include "pn_attend.h"
+#include "pn_launch.h"
 
 namespace pn {
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "pn_cache.h"
+#include "pn_launch.h"
 
 namespace pn {
 

@@ -7,7 +7,7 @@
 
 #include <atomic>
 
-#include "pn_common.h"
+#include "pn_launch.h"
 
 namespace pn {
 

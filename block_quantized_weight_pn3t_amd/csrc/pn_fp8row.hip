@@ -24,7 +24,7 @@
 
 #include <algorithm>
 
-#include "pn_common.h"
+#include "pn_launch.h"
 
 namespace pn {
 

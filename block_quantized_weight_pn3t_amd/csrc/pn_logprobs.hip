@@ -23,6 +23,7 @@
 #include "pn_arrive.h"
 #include "pn_cache.h"
 #include "pn_lanes.h"
+#include "pn_launch.h"
 
 namespace pn {
 

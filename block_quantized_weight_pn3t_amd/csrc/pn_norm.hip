@@ -21,6 +21,7 @@
 
 #include "pn_cache.h"
 #include "pn_lanes.h"
+#include "pn_launch.h"
 
 namespace pn {
 

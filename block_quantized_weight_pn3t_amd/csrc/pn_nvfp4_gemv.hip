@@ -14,7 +14,7 @@
 
 #include <algorithm>
 
-#include "pn_common.h"
+#include "pn_launch.h"
 
 namespace pn {
 

@@ -22,6 +22,7 @@
 
 #include "pn_arrive.h"
 #include "pn_cache.h"
+#include "pn_launch.h"
 
 namespace pn {
 
