@@ -90,7 +90,7 @@ __device__ __forceinline__ i32x4_t products(i32x4_t w, i32x4_t a, i32x4_t c)
 // ---- up to 32 tokens ------------------------------------------------------------------------------
 
 // EIGHTS: eights of tokens that are loaded, 1, 2 or 4. 34816 x 5120 at one token 29 us (6.1 TB/s of weights; a copy
-// reaches 4.9), 248320 x 5120 at four 214 (6.0), 5120 x 17408 at 13 16 (5.6).
+// reaches 4.9), at 16 31.7, 17 33.8, 32 38.3; 248320 x 5120 at four 214 (6.0); 5120 x 17408 at 13 16 (5.6), 32 21.8.
 template <int EIGHTS>
 struct Stream {
     static constexpr int WAVES = 4, ROWS = 32, TILES = (EIGHTS + 1) / 2;  // 16 tokens a tile
@@ -220,8 +220,9 @@ __device__ __forceinline__ void tile_of(const GemmArgs &A, int block, int blocks
     tm = __builtin_amdgcn_readfirstlane(band * kBand + in - column * high);
 }
 
-// SIZE x SIZE outputs a workgroup, a quarter each wave. A line of K takes 0.25 us (64, one workgroup a CU) and 0.5 (128): its
-// loads come from the Infinity Cache or memory, three or seven lines ahead, and 128 x 128 products need a fifth of it.
+// SIZE x SIZE outputs a workgroup, a quarter each wave. A line of K takes 0.25 us (64, one workgroup a CU) and 0.5 (128). Bound by
+// its loads, from the Infinity Cache or memory, three or seven lines ahead: 777 x 1024 x 5120 13.4 us, 12.1 without the products
+// and LDS reads of the loop, 9.8 without its loads; 300 x 5120 x 5120 20.0, 19.5, 11.3; 256 x 5120 x 17408 (128) 41.9, 42.1, 25.3.
 template <int SIZE, int STAGES_>
 struct Square {
     static constexpr int STAGE = 2 * SIZE * 128, LOADS = STAGE / 4096, STAGES = STAGES_;
@@ -391,7 +392,7 @@ constexpr int kLargeBytes = 8 * kUnit;
 // the wave's rows: (A0, B0), (A0, B1), (A1, B1), (A1, B0). What a turn reads can be loaded over two turns
 // later, when both waves have read it, and so each unit is loaded a step and a half before it is read.
 //
-// 8192 x 34816 x 5120, bf16: 1.09 ms, 2.67 POP/s; the matrix unit is busy 70 % of the time at the 1.75 GHz to which the
+// 8192 x 34816 x 5120, bf16: 1.07 to 1.11 ms over several boxes, 2.6 to 2.7 POP/s; the matrix unit is busy 70 % of the time at the 1.75 GHz to which the
 // chip lowers its clock (2.4 GHz with 16 tiles, where a line takes 0.96 us, 0.85 at the unit's rate). Without the
 // alternation, reads among the products and one barrier a turn, 1.21 ms; with 32x32x32 instructions, of which a turn has
 // two chains only, 1.34; without loads 0.90, without LDS reads 0.97.
@@ -600,9 +601,14 @@ static GemmCut gemm_cut(int64_t M, int64_t N, int64_t K)
     // What is estimated to be soonest, in us: rounds of workgroups, each some time a line and some to begin and end,
     // and the joining of K's parts. Measured for a line: 0.25 and 0.38 with one and two workgroups a CU (64), 0.5
     // (128; half of it where a last round leaves most CUs idle), 0.92 (256). So 64 x 1024 x 5120 is four parts in tiles
-    // of 64 (9.6 us; whole 12.3, in tiles of 128 20), 256 x 5120 x 17408 three in tiles of 128 (44; 86 whole, 59 in tiles
-    // of 64), 1024 x 5120 x 5120 tiles of 128 (45; 50 in those of 256), 2048 x 6144 x 5120 tiles of 256 (61; 92 in those
-    // of 128), 4096 x 5120 x 1024 too (36; 48), 777 x 5120 x 1024 tiles of 64 (16.1; 18.6 in those of 128).
+    // of 64 (9.3 us; whole 11.7, in tiles of 128 19.9), 256 x 5120 x 17408 three in tiles of 128 (42; 82 whole, 61 in tiles
+    // of 64), 1024 x 5120 x 5120 tiles of 128 (44; 49 in those of 256), 2048 x 6144 x 5120 tiles of 256 (57; 75 in those
+    // of 128), 4096 x 5120 x 1024 too (35; 45), 777 x 5120 x 1024 tiles of 64 (15.9; 18.5 in those of 128).
+    // The estimate has no term for the memory's rate, and a wide matrix that comes from memory gains nothing from idle CUs:
+    // 96 and 128 x 34816 x 5120 go to tiles of 128 (67.1 and 71.5 us) where those of 256 take 58.5 and 61.3, x 4096 56.8 and
+    // 59.9 for 47.4 and 49.4. Two parts in tiles of 128 would be sooner, too, than the tiles of 64 that 300 x 4096 x 6144,
+    // 8896 and 12288 go to (22.3, 29.4, 34.2; 20.2, 25.2, 29.1), tiles of 128 than those of 256 for 1500 x 5120 x 6144
+    // (56.6, 58.1).
     double best = INFINITY;
     for (const int size : {64, 128, 256}) {
         const int64_t t = up(M, size) * up(N, size), slots = size == 64 ? 2 * cus : cus;

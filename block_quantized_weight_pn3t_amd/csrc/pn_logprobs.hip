@@ -12,9 +12,11 @@
 // after the first batches is rare (about top / n of the logits at the n-th); then each lane offers its
 // best, and few are put in one by one, many are sorted among the lanes and merged.
 //
-// Memory bound for long rows: 2047 of 248,320 bf16 188 us with the five likeliest (5.4 TB/s; a copy reaches 4.9, the
-// exponentials and the rest would take about 150 by themselves). One row of fp32 13.2 us with 20, 8.3 with none, of
-// which a launch and a first load are 5. A wave reads batches of 4 KB, one ahead; a row is shared by up to 64
+// Memory bound for long rows: 2047 of 248,320 bf16 171 us with the five likeliest (169 to 181 over several boxes, 5.6 to 6.0
+// TB/s; a copy reaches 4.9, the exponentials and the rest would take about 150 by themselves). One row of fp32 13.6 us with 20,
+// 8.5 with none, of which a launch and a first load are 5. Between one row and some hundred the lists are what is far from the
+// floor: each wave begins one anew and raises its threshold by what it has seen itself (195 rows of 65,536 bf16 10.6 us with
+// none, 19.2 with five, 23.8 with 20). A wave reads batches of 4 KB, one ahead; a row is shared by up to 64
 // workgroups where there are few, and the last to arrive joins them (pn_arrive.h).
 #include <float.h>
 
@@ -197,7 +199,7 @@ struct Batch {
         for (int i = 0; i < LOADS; i++) {
             const int at = base + i * 64 * VEC;
             if (at + 64 * VEC <= V) {
-                // each line is read once (2047 rows of 248,320 bf16: 190 us, 204 by ordinary loads)
+                // each line is read once (2047 rows of 248,320 bf16, 5 likeliest: 177 us, 187 by ordinary loads)
                 v[i] = __builtin_nontemporal_load(reinterpret_cast<const EV *>(row + at + lane * VEC));
             } else {
 #pragma unroll
