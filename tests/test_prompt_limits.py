@@ -18,6 +18,11 @@ def test_logprobs_scales(V, scale, refused):
     assert (logp(V=V, stride=V, scale=scale, logits=0x1000, R=1, tokens=0x1002) == -2) == refused
 
 
+def test_logprobs_rows():
+    assert logp(R=1 << 25, tokens=0x1002) == -2 and logp(R=(1 << 25) - 1, tokens=0x1002) == -5
+    assert pn.logprobs_workspace_bytes(1 << 25, 5000, 2) == 0 < pn.logprobs_workspace_bytes((1 << 25) - 1, 5000, 2)
+
+
 @pytest.mark.parametrize("M,N,refused", [
     (64 * ((1 << 25) - 1), 1, True), (256 * ((1 << 23) - 1), 1, False), (1, 256 * ((1 << 23) - 1), False),
     (64 << 12, 64 << 13, True), (64 << 12, 64 * ((1 << 13) - 1), False)])
